@@ -14,6 +14,16 @@ step of the path runs in the library's kernels.
     ...  experts turn xd into y (same rows) ...
     out = moe_combine(shape, y, lay.dst_pos, gates, ws=ws, residual=x)
     moe_check(ws)                               # raises on a device-side error
+
+The rest of an expert layer, and what a training step takes back through it:
+
+    rule = ScoreRule(func="sigmoid", groups=8, top_groups=4, group_top=2, scale=2.5)
+    ids, gates = moe_route_scored(shape, logits, rule, bias, ws=ws)
+    h = moe_expert_matmul(shape, xd, w1, lay.counts, lay.expert_off, ws=ws, act="swiglu")
+    y = moe_expert_matmul(shape, h, w2, lay.counts, lay.expert_off, ws=ws)
+    g = moe_expert_matmul_backward(shape, grad_y, h, w2, lay.counts, lay.expert_off, ws=ws)
+    grad_y, grad_gates = moe_combine_backward(shape, grad_out, y, lay.dst_pos, gates, ws=ws)
+    grad_logits = moe_route_scored_backward(shape, logits, rule, ids, grad_gates, ws=ws)
 """
 from __future__ import annotations
 
@@ -31,7 +41,9 @@ __all__ = ["MoeShape", "Workspace", "Layout", "LayoutSrc", "MoeError", "moe_rout
            "moe_layout_remote_first", "moe_route_round_robin",
            "moe_route_layout", "moe_route_layout_dispatch",
            "moe_dispatch", "moe_combine", "moe_get_device_error", "moe_check",
-           "moe_layout_rows", "moe_workspace_bytes"]
+           "moe_layout_rows", "moe_workspace_bytes", "ScoreRule", "ExpertGrads",
+           "moe_route_scored", "moe_route_scored_backward", "moe_expert_matmul",
+           "moe_expert_matmul_backward", "moe_combine_backward"]
 
 
 @dataclasses.dataclass(frozen=True)
@@ -396,6 +408,218 @@ def moe_combine(shape: MoeShape, y: torch.Tensor, dst_pos: torch.Tensor, gates: 
         _ptr(out, "out", torch.bfloat16, (T, H)), ws.ptr, ws.nbytes, _stream(dev))
     _check(st, "moe_combine")
     return out
+
+
+class _On:
+    """The device of a call: its index, and a guard that makes it current for
+    the launch where it is not already."""
+
+    def __init__(self, ws: Workspace, *tensors):
+        self.device = ws.buf.device
+        for t in tensors:
+            if t is not None and t.device != self.device:
+                raise ValueError(f"every tensor must be on the workspace's device {self.device}, "
+                                 f"got {t.device}")
+
+    def __enter__(self):
+        index = self.device.index
+        self.before = torch.cuda.current_device()
+        if index != self.before:
+            torch.cuda.set_device(index)
+        else:
+            self.before = None
+        return torch.cuda.current_stream(index).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.before is not None:
+            torch.cuda.set_device(self.before)
+        return False
+
+
+@dataclasses.dataclass(frozen=True)
+class ScoreRule:
+    """How moe_route_scored scores and chooses: `func` "softmax" or "sigmoid";
+    each token keeps the `top_groups` best of `groups` groups of experts, a
+    group scored by the sum of its `group_top` (1 or 2) largest keys; the gates
+    are multiplied by `scale`."""
+    func: str = "softmax"
+    groups: int = 1
+    top_groups: int = 1
+    group_top: int = 1
+    scale: float = 1.0
+
+    def c(self) -> _binding.MoeScoreC:
+        if self.func not in _binding.MOE_SCORES:
+            raise ValueError(f"func must be one of {sorted(_binding.MOE_SCORES)}, got {self.func!r}")
+        return _binding.MoeScoreC(_binding.MOE_SCORES[self.func], self.groups, self.top_groups,
+                                  self.group_top, self.scale)
+
+
+def moe_route_scored(shape: MoeShape, logits: torch.Tensor, rule: ScoreRule,
+                     bias: Optional[torch.Tensor] = None, *, ws: Workspace,
+                     ids: Optional[torch.Tensor] = None, gates: Optional[torch.Tensor] = None):
+    """Top-k by sigmoid or softmax scores plus bias, among the best groups of
+    experts; returns (ids int32 [T,k], gates fp32 [T,k])."""
+    T, E, k = shape.tokens, shape.experts, shape.k
+    dev = logits.device
+    if ids is None:
+        ids = torch.empty((T, k), dtype=torch.int32, device=dev)
+    if gates is None:
+        gates = torch.empty((T, k), dtype=torch.float32, device=dev)
+    with _On(ws, logits, bias, ids, gates) as stream:
+        st = _binding.lib().moe_route_scored(
+            ctypes.byref(shape.c()), _ptr(logits, "logits", torch.float32, (T, E)),
+            _ptr(bias, "bias", torch.float32, (E,)), ctypes.byref(rule.c()),
+            _ptr(ids, "ids", torch.int32, (T, k)), _ptr(gates, "gates", torch.float32, (T, k)),
+            ws.ptr, ws.nbytes, stream)
+    _check(st, "moe_route_scored")
+    return ids, gates
+
+
+def moe_route_scored_backward(shape: MoeShape, logits: torch.Tensor, rule: ScoreRule,
+                              ids: torch.Tensor, grad_gates: torch.Tensor, *, ws: Workspace,
+                              grad_logits: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """Gradient of the logits through moe_route_scored's gates, fp32 [T,E]."""
+    T, E, k = shape.tokens, shape.experts, shape.k
+    if grad_logits is None:
+        grad_logits = torch.empty((T, E), dtype=torch.float32, device=logits.device)
+    with _On(ws, logits, ids, grad_gates, grad_logits) as stream:
+        st = _binding.lib().moe_route_scored_backward(
+            ctypes.byref(shape.c()), _ptr(logits, "logits", torch.float32, (T, E)),
+            ctypes.byref(rule.c()), _ptr(ids, "ids", torch.int32, (T, k)),
+            _ptr(grad_gates, "grad_gates", torch.float32, (T, k)),
+            _ptr(grad_logits, "grad_logits", torch.float32, (T, E)), ws.ptr, ws.nbytes, stream)
+    _check(st, "moe_route_scored_backward")
+    return grad_logits
+
+
+def _act(act: str) -> int:
+    if act not in _binding.MOE_ACTS:
+        raise ValueError(f"act must be one of {sorted(_binding.MOE_ACTS)}, got {act!r}")
+    return _binding.MOE_ACTS[act]
+
+
+def _features(w: torch.Tensor, E: int, act: str):
+    """(in_features, out_features, Wd) of a weight tensor [E, Wd, in_features]."""
+    if w.dim() != 3 or w.shape[0] != E:
+        raise ValueError(f"w must have shape [{E}, features, in_features], got {tuple(w.shape)}")
+    wide = w.shape[1]
+    if act == "swiglu":
+        if wide % 2:
+            raise ValueError("swiglu needs w with gate and up halves: an even number of rows")
+        return w.shape[2], wide // 2, wide
+    return w.shape[2], wide, wide
+
+
+def moe_expert_matmul(shape: MoeShape, x: torch.Tensor, w: torch.Tensor,
+                      counts: Optional[torch.Tensor] = None,
+                      expert_off: Optional[torch.Tensor] = None, *, ws: Workspace,
+                      bias: Optional[torch.Tensor] = None, act: str = "none",
+                      residual: Optional[torch.Tensor] = None,
+                      out: Optional[torch.Tensor] = None,
+                      pre: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """act(x[p] W_e^T + bias_e) + residual[p] for every row p that holds a token
+    of expert e, bf16 [N, F].  x bf16 [N, K]; w bf16 [E, F, K], or [E, 2F, K]
+    with act "swiglu" (gate rows, then up rows); counts and expert_off from the
+    layout, or neither for a dense product (one expert, every row).  `pre` bf16
+    [N, F or 2F] receives the pre-activations that the backward call reads.
+    Rows that hold no token are left as they are."""
+    a = _act(act)
+    E, N = shape.experts, shape.rows
+    K, F, wide = _features(w, E, act)
+    bf16 = torch.bfloat16
+    if out is None:
+        out = torch.empty((N, F), dtype=bf16, device=x.device)
+    with _On(ws, x, w, counts, expert_off, bias, residual, out, pre) as stream:
+        st = _binding.lib().moe_expert_matmul(
+            ctypes.byref(shape.c()), K, F, a, _ptr(x, "x", bf16, (N, K)), _ptr(w, "w", bf16),
+            _ptr(bias, "bias", torch.float32, (E, wide)),
+            _ptr(counts, "counts", torch.int32, (E,)),
+            _ptr(expert_off, "expert_off", torch.int32, (E + 1,)),
+            _ptr(residual, "residual", bf16, (N, F)), _ptr(out, "out", bf16, (N, F)),
+            _ptr(pre, "pre", bf16, (N, wide)), ws.ptr, ws.nbytes, stream)
+    _check(st, "moe_expert_matmul")
+    return out
+
+
+@dataclasses.dataclass
+class ExpertGrads:
+    grad_x: Optional[torch.Tensor]     # bf16 [N, K]
+    grad_w: Optional[torch.Tensor]     # bf16 [E, Wd, K]
+    grad_bias: Optional[torch.Tensor]  # fp32 [E, Wd]
+    grad_pre: Optional[torch.Tensor]   # bf16 [N, Wd] (None with act "none")
+
+
+def moe_expert_matmul_backward(shape: MoeShape, grad_out: torch.Tensor, x: torch.Tensor,
+                               w: torch.Tensor, counts: Optional[torch.Tensor] = None,
+                               expert_off: Optional[torch.Tensor] = None, *, ws: Workspace,
+                               act: str = "none", pre: Optional[torch.Tensor] = None,
+                               need_x: bool = True, need_w: bool = True, need_bias: bool = False,
+                               grad_pre: Optional[torch.Tensor] = None,
+                               grad_x: Optional[torch.Tensor] = None,
+                               grad_w: Optional[torch.Tensor] = None,
+                               grad_bias: Optional[torch.Tensor] = None) -> ExpertGrads:
+    """Gradients of moe_expert_matmul: of x, w and the bias (each where asked
+    for, or where a buffer is given), with `pre` as the forward call wrote it.
+    The residual's gradient is grad_out.  Rows of grad_x and grad_pre that hold
+    no token are left as they are."""
+    a = _act(act)
+    E, N = shape.experts, shape.rows
+    K, F, wide = _features(w, E, act)
+    dev, bf16 = x.device, torch.bfloat16
+    if grad_x is None and need_x:
+        grad_x = torch.empty((N, K), dtype=bf16, device=dev)
+    if grad_w is None and need_w:
+        grad_w = torch.empty((E, wide, K), dtype=bf16, device=dev)
+    if grad_bias is None and need_bias:
+        grad_bias = torch.empty((E, wide), dtype=torch.float32, device=dev)
+    if act == "none":
+        pre = grad_pre = None
+    elif grad_pre is None:
+        grad_pre = torch.empty((N, wide), dtype=bf16, device=dev)
+    scratch, nbytes = None, 0
+    cs = shape.c()
+    with _On(ws, grad_out, x, w, counts, expert_off, pre, grad_pre, grad_x, grad_w,
+             grad_bias) as stream:
+        if grad_bias is not None:
+            nbytes = _binding.lib().moe_expert_matmul_backward_scratch_bytes(ctypes.byref(cs), F, a)
+            scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+        st = _binding.lib().moe_expert_matmul_backward(
+            ctypes.byref(cs), K, F, a, _ptr(grad_out, "grad_out", bf16, (N, F)),
+            _ptr(x, "x", bf16, (N, K)), _ptr(w, "w", bf16), _ptr(pre, "pre", bf16, (N, wide)),
+            _ptr(counts, "counts", torch.int32, (E,)),
+            _ptr(expert_off, "expert_off", torch.int32, (E + 1,)),
+            _ptr(grad_pre, "grad_pre", bf16, (N, wide)), _ptr(grad_x, "grad_x", bf16, (N, K)),
+            _ptr(grad_w, "grad_w", bf16, (E, wide, K)),
+            _ptr(grad_bias, "grad_bias", torch.float32, (E, wide)),
+            None if scratch is None else scratch.data_ptr(), nbytes, ws.ptr, ws.nbytes, stream)
+    _check(st, "moe_expert_matmul_backward")
+    return ExpertGrads(grad_x, grad_w, grad_bias, grad_pre)
+
+
+def moe_combine_backward(shape: MoeShape, grad_out: torch.Tensor, y: torch.Tensor,
+                         dst_pos: torch.Tensor, gates: torch.Tensor, *, ws: Workspace,
+                         grad_y: Optional[torch.Tensor] = None,
+                         grad_gates: Optional[torch.Tensor] = None):
+    """Gradients of moe_combine: (grad_y bf16 [N,H], grad_gates fp32 [T,k]).
+    Rows of grad_y that no slot maps to are left as they are; the gradients of
+    shared and residual are grad_out.  (The gradient of moe_dispatch is
+    moe_combine with gates of one.)"""
+    T, H, k = shape.tokens, shape.hidden, shape.k
+    N = shape.rows
+    if grad_y is None:
+        grad_y = torch.empty((N, H), dtype=torch.bfloat16, device=y.device)
+    if grad_gates is None:
+        grad_gates = torch.empty((T, k), dtype=torch.float32, device=y.device)
+    with _On(ws, grad_out, y, dst_pos, gates, grad_y, grad_gates) as stream:
+        st = _binding.lib().moe_combine_backward(
+            ctypes.byref(shape.c()), _ptr(grad_out, "grad_out", torch.bfloat16, (T, H)),
+            _ptr(y, "y", torch.bfloat16, (N, H)), _ptr(dst_pos, "dst_pos", torch.int32, (T, k)),
+            _ptr(gates, "gates", torch.float32, (T, k)),
+            _ptr(grad_y, "grad_y", torch.bfloat16, (N, H)),
+            _ptr(grad_gates, "grad_gates", torch.float32, (T, k)), ws.ptr, ws.nbytes, stream)
+    _check(st, "moe_combine_backward")
+    return grad_y, grad_gates
 
 
 def moe_get_device_error(ws: Workspace):

@@ -24,6 +24,9 @@ MOE_F_RENORM = 0x1
 MOE_F_FP8 = 0x2
 MOE_F_SRC_LAYOUT = 0x4
 
+MOE_SCORES = {"softmax": 0, "sigmoid": 1}
+MOE_ACTS = {"none": 0, "relu": 1, "gelu": 2, "silu": 3, "swiglu": 4}
+
 # Every extern "C" symbol of include/moe_route07.h.
 EXPORTS = (
     "moe_abi_version", "moe_status_string", "moe_layout_rows", "moe_workspace_bytes",
@@ -31,7 +34,9 @@ EXPORTS = (
     "moe_get_device_error", "moe_layout_noalloc", "moe_route_layout",
     "moe_route_layout_dispatch", "moe_layout_src", "moe_route_limited",
     "moe_bias_update", "moe_layout_remote_first", "moe_route_round_robin",
-    "moe_selftest_wait_timeout",
+    "moe_selftest_wait_timeout", "moe_route_scored", "moe_route_scored_backward",
+    "moe_expert_matmul", "moe_expert_matmul_backward",
+    "moe_expert_matmul_backward_scratch_bytes", "moe_combine_backward",
 )
 
 
@@ -40,6 +45,12 @@ class MoeShapeC(ctypes.Structure):
                 ("experts", ctypes.c_int32), ("k", ctypes.c_int32), ("ranks", ctypes.c_int32),
                 ("capacity", ctypes.c_int32), ("align", ctypes.c_int32),
                 ("flags", ctypes.c_uint32)]
+
+
+class MoeScoreC(ctypes.Structure):
+    _fields_ = [("func", ctypes.c_int32), ("groups", ctypes.c_int32),
+                ("top_groups", ctypes.c_int32), ("group_top", ctypes.c_int32),
+                ("scale", ctypes.c_double)]
 
 
 class MoeError(RuntimeError):
@@ -99,6 +110,20 @@ def lib(path: str = None):
     L.moe_layout_src.restype = i32
     L.moe_layout_noalloc.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, vp]
     L.moe_layout_noalloc.restype = i32
+    rp = ctypes.POINTER(MoeScoreC)
+    L.moe_route_scored.argtypes = [sp, vp, vp, rp, vp, vp, vp, sz, vp]
+    L.moe_route_scored.restype = i32
+    L.moe_route_scored_backward.argtypes = [sp, vp, rp, vp, vp, vp, vp, sz, vp]
+    L.moe_route_scored_backward.restype = i32
+    L.moe_expert_matmul.argtypes = [sp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_expert_matmul.restype = i32
+    L.moe_expert_matmul_backward.argtypes = [sp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp, vp, vp,
+                                             vp, vp, sz, vp, sz, vp]
+    L.moe_expert_matmul_backward.restype = i32
+    L.moe_expert_matmul_backward_scratch_bytes.argtypes = [sp, i32, i32]
+    L.moe_expert_matmul_backward_scratch_bytes.restype = sz
+    L.moe_combine_backward.argtypes = [sp, vp, vp, vp, vp, vp, vp, vp, sz, vp]
+    L.moe_combine_backward.restype = i32
     L.moe_get_device_error.argtypes = [vp, ctypes.POINTER(i32), vp]
     L.moe_get_device_error.restype = i32
     if path is None:

@@ -403,6 +403,213 @@ moe_status_t moe_combine(const moe_shape_t* shape, const void* y, const int32_t*
                                        out, static_cast<WsHeader*>(ws), shape->capacity > 0));
 }
 
+moe_status_t moe_combine_backward(const moe_shape_t* shape, const void* grad_out, const void* y,
+                                  const int32_t* dst_pos, const float* gates, void* grad_y,
+                                  float* grad_gates, void* ws, size_t ws_bytes,
+                                  moe_stream_t stream) {
+  if (!shape_ok(shape)) return MOE_ERR_INVALID_ARG;
+  if (shape->tokens > 0 && (grad_out == nullptr || dst_pos == nullptr || gates == nullptr ||
+                            grad_gates == nullptr || y == nullptr || grad_y == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(grad_out, 16) || !aligned(y, 16) || !aligned(grad_y, 16) || !aligned(dst_pos, 4) ||
+      !aligned(gates, 4) || !aligned(grad_gates, 4))
+    return MOE_ERR_INVALID_ARG;
+  moe_status_t st = ws_ok(shape, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  if (shape->tokens == 0) return MOE_OK;
+  return from_cuda(moe::launch_combine_backward(env_of(stream), grad_out, y, dst_pos, gates,
+                                                shape->tokens, shape->hidden, shape->k,
+                                                rows_of(shape), grad_y, grad_gates,
+                                                static_cast<WsHeader*>(ws)));
+}
+
+}  // extern "C"
+
+namespace {
+
+bool rule_ok(const moe_shape_t* s, const moe_score_t* r, moe::ScoreRule* out) {
+  if (r == nullptr) return false;
+  if (r->func != MOE_SCORE_SOFTMAX && r->func != MOE_SCORE_SIGMOID) return false;
+  if (r->groups < 1 || r->groups > 64 || (s->experts % r->groups) != 0) return false;
+  const int size = s->experts / r->groups;
+  if (r->top_groups < 1 || r->top_groups > r->groups) return false;
+  if ((int64_t)r->top_groups * size < s->k) return false;
+  if (r->group_top < 1 || r->group_top > 2 || r->group_top > size) return false;
+  if (!std::isfinite(r->scale) || r->scale <= 0.0) return false;
+  out->softmax = r->func == MOE_SCORE_SOFTMAX ? 1 : 0;
+  out->groups = r->groups;
+  out->top_groups = r->top_groups;
+  out->group_top = r->group_top;
+  out->renorm = (s->flags & MOE_F_RENORM) ? 1 : 0;
+  out->scale = r->scale;
+  return true;
+}
+
+int wide_of(int32_t out_features, int32_t act) {
+  return act == MOE_ACT_SWIGLU ? 2 * out_features : out_features;
+}
+
+// The checks the experts' products share.
+moe_status_t experts_ok(const moe_shape_t* s, int32_t in, int32_t out, int32_t act,
+                        const int32_t* counts, const int32_t* expert_off) {
+  if (!shape_ok(s) || src_layout(s)) return MOE_ERR_INVALID_ARG;
+  if (in < 8 || (in % 8) != 0 || in > 65536) return MOE_ERR_INVALID_ARG;
+  if (out < 8 || (out % 8) != 0 || out > 65536) return MOE_ERR_INVALID_ARG;
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU) return MOE_ERR_INVALID_ARG;
+  if ((counts == nullptr) != (expert_off == nullptr)) return MOE_ERR_INVALID_ARG;
+  if (counts == nullptr && (s->experts != 1 || s->capacity != 0 || s->align != 1))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(counts, 4) || !aligned(expert_off, 4)) return MOE_ERR_INVALID_ARG;
+  if (!moe::expert_tiles_fit(int64_t(s->tokens) * s->k, s->experts, in, wide_of(out, act)))
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+moe::ExpertMatmul experts_of(const moe_shape_t* s, int32_t in, int32_t out, int32_t act,
+                             const void* x, const void* w, const int32_t* counts,
+                             const int32_t* expert_off, void* ws) {
+  moe::ExpertMatmul a = {};
+  a.x = x;
+  a.w = w;
+  a.counts = counts;
+  a.expert_off = expert_off;
+  a.hdr = static_cast<WsHeader*>(ws);
+  a.N = rows_of(s);
+  a.assignments = int64_t(s->tokens) * s->k;
+  a.E = s->experts;
+  a.capacity = s->capacity;
+  a.in_features = in;
+  a.out_features = out;
+  a.act = act;
+  return a;
+}
+
+}  // namespace
+
+extern "C" {
+
+moe_status_t moe_route_scored(const moe_shape_t* shape, const float* logits, const float* bias,
+                              const moe_score_t* rule, int32_t* ids, float* gates, void* ws,
+                              size_t ws_bytes, moe_stream_t stream) {
+  moe::ScoreRule r;
+  if (!shape_ok(shape) || !rule_ok(shape, rule, &r)) return MOE_ERR_INVALID_ARG;
+  if (shape->tokens > 0 && (logits == nullptr || ids == nullptr || gates == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(ids, 4) || !aligned(gates, 4))
+    return MOE_ERR_INVALID_ARG;
+  moe_status_t st = ws_ok(shape, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  if (shape->tokens == 0) return MOE_OK;
+  return from_cuda(moe::launch_route_scored(env_of(stream), logits, bias, shape->tokens,
+                                            shape->experts, shape->k, r, ids, gates,
+                                            static_cast<WsHeader*>(ws)));
+}
+
+moe_status_t moe_route_scored_backward(const moe_shape_t* shape, const float* logits,
+                                       const moe_score_t* rule, const int32_t* ids,
+                                       const float* grad_gates, float* grad_logits, void* ws,
+                                       size_t ws_bytes, moe_stream_t stream) {
+  moe::ScoreRule r;
+  if (!shape_ok(shape) || !rule_ok(shape, rule, &r)) return MOE_ERR_INVALID_ARG;
+  if (shape->tokens > 0 && (logits == nullptr || ids == nullptr || grad_gates == nullptr ||
+                            grad_logits == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(logits, 4) || !aligned(ids, 4) || !aligned(grad_gates, 4) ||
+      !aligned(grad_logits, 4))
+    return MOE_ERR_INVALID_ARG;
+  moe_status_t st = ws_ok(shape, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  if (shape->tokens == 0) return MOE_OK;
+  return from_cuda(moe::launch_route_scored_backward(
+      env_of(stream), logits, ids, grad_gates, shape->tokens, shape->experts, shape->k, r,
+      grad_logits, static_cast<WsHeader*>(ws)));
+}
+
+moe_status_t moe_expert_matmul(const moe_shape_t* shape, int32_t in_features,
+                               int32_t out_features, int32_t act, const void* x, const void* w,
+                               const float* bias, const int32_t* counts,
+                               const int32_t* expert_off, const void* residual, void* out,
+                               void* pre, void* ws, size_t ws_bytes, moe_stream_t stream) {
+  moe_status_t st = experts_ok(shape, in_features, out_features, act, counts, expert_off);
+  if (st != MOE_OK) return st;
+  if (shape->tokens > 0 && (x == nullptr || w == nullptr || out == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (!aligned(x, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(pre, 16) ||
+      !aligned(residual, 16) || !aligned(bias, 4))
+    return MOE_ERR_INVALID_ARG;
+  st = ws_ok(shape, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  if (shape->tokens == 0) return MOE_OK;
+  moe::ExpertMatmul a = experts_of(shape, in_features, out_features, act, x, w, counts,
+                                   expert_off, ws);
+  a.bias = bias;
+  a.residual = residual;
+  a.out = out;
+  a.pre = pre;
+  return from_cuda(moe::launch_expert_matmul(env_of(stream), a));
+}
+
+size_t moe_expert_matmul_backward_scratch_bytes(const moe_shape_t* shape, int32_t out_features,
+                                                int32_t act) {
+  if (!shape_ok(shape) || src_layout(shape)) return 0;
+  if (out_features < 8 || (out_features % 8) != 0 || out_features > 65536) return 0;
+  if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU) return 0;
+  const int64_t tiles = moe::expert_act_tiles(int64_t(shape->tokens) * shape->k, shape->experts);
+  return size_t(tiles > 0 ? tiles : 1) * wide_of(out_features, act) * sizeof(float);
+}
+
+moe_status_t moe_expert_matmul_backward(const moe_shape_t* shape, int32_t in_features,
+                                        int32_t out_features, int32_t act, const void* grad_out,
+                                        const void* x, const void* w, const void* pre,
+                                        const int32_t* counts, const int32_t* expert_off,
+                                        void* grad_pre, void* grad_x, void* grad_w,
+                                        float* grad_bias, void* scratch, size_t scratch_bytes,
+                                        void* ws, size_t ws_bytes, moe_stream_t stream) {
+  moe_status_t st = experts_ok(shape, in_features, out_features, act, counts, expert_off);
+  if (st != MOE_OK) return st;
+  const bool rows = shape->tokens > 0;
+  if (rows && grad_out == nullptr) return MOE_ERR_INVALID_ARG;
+  if (rows && act != MOE_ACT_NONE && (pre == nullptr || grad_pre == nullptr))
+    return MOE_ERR_INVALID_ARG;
+  if (rows && grad_x != nullptr && w == nullptr) return MOE_ERR_INVALID_ARG;
+  if (rows && grad_w != nullptr && x == nullptr) return MOE_ERR_INVALID_ARG;
+  const void* ptrs[] = {grad_out, x, w, pre, grad_pre, grad_x, grad_w, scratch};
+  for (const void* p : ptrs)
+    if (!aligned(p, 16)) return MOE_ERR_INVALID_ARG;
+  if (!aligned(grad_bias, 4)) return MOE_ERR_INVALID_ARG;
+  if (grad_bias != nullptr &&
+      (scratch == nullptr ||
+       scratch_bytes < moe_expert_matmul_backward_scratch_bytes(shape, out_features, act)))
+    return MOE_ERR_WORKSPACE;
+  st = ws_ok(shape, ws, ws_bytes);
+  if (st != MOE_OK) return st;
+  const int wide = wide_of(out_features, act);
+  if (!rows) {  // no rows: the sums over rows are zero
+    const size_t cells = (size_t)shape->experts * wide;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    if (grad_w != nullptr &&
+        cudaMemsetAsync(grad_w, 0, cells * in_features * 2, s) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    if (grad_bias != nullptr &&
+        cudaMemsetAsync(grad_bias, 0, cells * sizeof(float), s) != cudaSuccess)
+      return MOE_ERR_CUDA;
+    return MOE_OK;
+  }
+  const moe::LaunchEnv env = env_of(stream);
+  const moe::ExpertMatmul a = experts_of(shape, in_features, out_features, act, x, w, counts,
+                                         expert_off, ws);
+  const void* dz = act == MOE_ACT_NONE ? grad_out : grad_pre;
+  cudaError_t err = cudaSuccess;
+  if (act != MOE_ACT_NONE || grad_bias != nullptr)
+    err = moe::launch_expert_act_backward(env, a, grad_out, pre, grad_pre,
+                                          static_cast<float*>(scratch), grad_bias);
+  if (err == cudaSuccess && grad_x != nullptr)
+    err = moe::launch_expert_grad_rows(env, a, dz, grad_x);
+  if (err == cudaSuccess && grad_w != nullptr)
+    err = moe::launch_expert_grad_weights(env, a, dz, grad_w);
+  return from_cuda(err);
+}
+
 moe_status_t moe_selftest_wait_timeout(void* ws, uint32_t timeout_us, moe_stream_t stream) {
   if (ws == nullptr || !aligned(ws, 16)) return MOE_ERR_WORKSPACE;
   if (timeout_us < 1u || timeout_us > 2000000u) return MOE_ERR_INVALID_ARG;

@@ -184,6 +184,56 @@ cudaError_t launch_route_round_robin(const LaunchEnv& env, int T, int E, int k, 
 cudaError_t launch_bias_update(const LaunchEnv& env, const int32_t* counts, int E,
                                int64_t assignments, float gamma, float* bias);
 
+// Routing by scores (host-checked rule): groups <= 64, top_groups <= groups,
+// group_top 1 or 2.
+struct ScoreRule {
+  int softmax;     // else sigmoid
+  int groups;
+  int top_groups;
+  int group_top;
+  int renorm;
+  double scale;
+};
+cudaError_t launch_route_scored(const LaunchEnv& env, const float* logits, const float* bias, int T,
+                                int E, int k, const ScoreRule& rule, int32_t* ids, float* gates,
+                                WsHeader* hdr);
+cudaError_t launch_route_scored_backward(const LaunchEnv& env, const float* logits,
+                                         const int32_t* ids, const float* grad_gates, int T, int E,
+                                         int k, const ScoreRule& rule, float* grad_logits,
+                                         WsHeader* hdr);
+
+cudaError_t launch_combine_backward(const LaunchEnv& env, const void* grad_out, const void* y,
+                                    const int32_t* dst_pos, const float* gates, int T, int H, int k,
+                                    int64_t N, void* grad_y, float* grad_gates, WsHeader* hdr);
+
+// The experts' products.  assignments bounds the rows that hold a token (T*k,
+// or E*C with a capacity, if smaller): grids are sized from it, the segments
+// themselves are read on the device.
+struct ExpertMatmul {
+  const void* x;
+  const void* w;
+  const float* bias;
+  const int32_t* counts;      // NULL (E = 1): every row
+  const int32_t* expert_off;
+  const void* residual;
+  void* out;
+  void* pre;
+  WsHeader* hdr;
+  int64_t N, assignments;
+  int E, capacity, in_features, out_features, act;
+};
+bool expert_tiles_fit(int64_t assignments, int E, int in, int wide);
+cudaError_t launch_expert_matmul(const LaunchEnv& env, const ExpertMatmul& a);
+cudaError_t launch_expert_grad_rows(const LaunchEnv& env, const ExpertMatmul& a, const void* dz,
+                                    void* grad_x);
+cudaError_t launch_expert_grad_weights(const LaunchEnv& env, const ExpertMatmul& a, const void* dz,
+                                       void* grad_w);
+// Rows of a tile of the activation's gradient, and the most tiles there can be.
+constexpr int kActRows = 64;
+int64_t expert_act_tiles(int64_t assignments, int E);
+cudaError_t launch_expert_act_backward(const LaunchEnv& env, const ExpertMatmul& a, const void* dy,
+                                       const void* z, void* dz, float* partial, float* grad_bias);
+
 // sparse: most slots may be dropped (capacity mode)
 cudaError_t launch_combine(const LaunchEnv& env, const void* y, const int32_t* dst_pos,
                            const float* gates, const void* shared, const void* residual, int T,

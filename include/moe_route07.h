@@ -19,6 +19,12 @@
  *   "Mixture-of-experts acceleration through overlap" (thecoregrid): the
  *      remote-owner-aligned layout (every row band bound to one destination).
  *
+ * What a layer needs around the four steps: routing by sigmoid or softmax
+ * scores with groups of experts (moe_route_scored), the experts' matrix
+ * products on the layout's rows (moe_expert_matmul), and the gradients a
+ * training step takes (moe_route_scored_backward, moe_expert_matmul_backward,
+ * moe_combine_backward).
+ *
  * Besides the four steps (moe_route, moe_layout, moe_dispatch, moe_combine,
  * and the fused moe_route_layout / moe_route_layout_dispatch): the
  * per-source-rank layout of a ragged exchange (moe_layout_src), rank-limited
@@ -301,6 +307,125 @@ moe_status_t moe_route_layout_dispatch(const moe_shape_t* shape, const float* lo
 moe_status_t moe_combine(const moe_shape_t* shape, const void* y, const int32_t* dst_pos,
                          const float* gates, const void* shared, const void* residual,
                          void* out, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Routing by scores.  For each token t:
+ *   score[e] = sigmoid(logits[t,e]), or softmax(logits[t,:])[e]
+ *   key[e]   = score[e] + bias[e]          (bias NULL = 0)
+ *   experts g*(E/groups) .. (g+1)*(E/groups)-1 form group g; its score is the
+ *   sum of its group_top largest keys; the top_groups best groups are kept
+ *   (equal scores: the lower group)
+ *   ids[t,j] = the expert with the j-th largest key of the kept groups (equal
+ *              keys: the lower expert)
+ *   gates[t,j] = scale * score[ids[t,j]], divided by the sum of the k chosen
+ *                scores with MOE_F_RENORM (0 where that sum is 0); the bias
+ *                never enters the gates.
+ * Keys are those of binary64 arithmetic, whichever way the kernel decides
+ * them.  A bias of -inf takes an expert out of the choice unless nothing else
+ * is left.  A key that is NaN or +inf sets MOE_ERR_DEVICE_NAN; that token gets
+ * the experts 0..k-1 with gates of zero.
+ *   func       MOE_SCORE_SOFTMAX or MOE_SCORE_SIGMOID
+ *   groups     divides E, 1..64
+ *   top_groups 1..groups, with k <= top_groups * (E/groups)
+ *   group_top  1 or 2, at most E/groups
+ *   scale      finite, > 0
+ * Buffers as moe_route. */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+typedef struct {
+  int32_t func, groups, top_groups, group_top;
+  double scale;
+} moe_score_t;
+moe_status_t moe_route_scored(const moe_shape_t* shape, const float* logits, const float* bias,
+                              const moe_score_t* rule, int32_t* ids, float* gates, void* ws,
+                              size_t ws_bytes, moe_stream_t stream);
+
+/* Gradient of the logits through the gates of moe_route_scored (the choice
+ * itself has none).  ids are the chosen experts, grad_gates fp32 [T,k];
+ * grad_logits fp32 [T,E] is written whole (zeros where there is no gradient).
+ * An expert that appears in two slots of a token gets the sum of their parts;
+ * an id outside [0,E) sets MOE_ERR_DEVICE_RANGE and its slot has no gradient
+ * and no share in the renormalisation. */
+moe_status_t moe_route_scored_backward(const moe_shape_t* shape, const float* logits,
+                                       const moe_score_t* rule, const int32_t* ids,
+                                       const float* grad_gates, float* grad_logits, void* ws,
+                                       size_t ws_bytes, moe_stream_t stream);
+
+/* The experts' matrix product on the rows of a layout.  For every row p that
+ * holds a token of expert e:
+ *   z[p,:] = x[p,:] W_e^T + bias_e
+ *   y[p,:] = act(z[p,:]) + residual[p,:]
+ *   act: none, relu, gelu (by erf), silu, or swiglu: silu(z[:F]) * z[F:]
+ * with F = out_features and Wd = F, or 2F with swiglu (rows 0..F-1 of a weight
+ * matrix are the gate half, F..2F-1 the up half).
+ *   x          bf16 [N,in_features]
+ *   w          bf16 [E,Wd,in_features]
+ *   counts     int32 [E], expert_off int32 [E+1]: as moe_layout or
+ *              moe_layout_remote_first wrote them (only expert_off[0..E-1] is
+ *              read).  Both NULL: E must be 1 and the layout dropless with
+ *              align 1, and every row belongs to it (a dense product).
+ *   bias       fp32 [E,Wd] or NULL
+ *   residual   bf16 [N,F] or NULL; may be `out` itself
+ *   out        bf16 [N,F]
+ *   pre        bf16 [N,Wd] or NULL: z, which the backward call reads
+ * N = moe_layout_rows(shape).  The features are multiples of 8, at most 65536;
+ * shape->hidden and MOE_F_FP8 play no part.  Sums, bias, activation and
+ * residual are fp32; out and pre are each rounded once.  Rows that hold no
+ * token are neither read into a sum nor written.  bf16 buffers 16-byte, the
+ * others 4-byte aligned; out and pre overlap no input except as said.
+ * MOE_F_SRC_LAYOUT returns MOE_ERR_INVALID_ARG; more than 2^31 output tiles
+ * MOE_ERR_UNSUPPORTED.  A segment outside the N rows sets
+ * MOE_ERR_DEVICE_RANGE (detail: the expert) and is skipped; counts that sum to
+ * more than T*k set it with detail E, and nothing is computed. */
+#define MOE_ACT_NONE 0
+#define MOE_ACT_RELU 1
+#define MOE_ACT_GELU 2
+#define MOE_ACT_SILU 3
+#define MOE_ACT_SWIGLU 4
+moe_status_t moe_expert_matmul(const moe_shape_t* shape, int32_t in_features,
+                               int32_t out_features, int32_t act, const void* x, const void* w,
+                               const float* bias, const int32_t* counts,
+                               const int32_t* expert_off, const void* residual, void* out,
+                               void* pre, void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Bytes of scratch moe_expert_matmul_backward needs for grad_bias; 0 for
+ * invalid arguments. */
+size_t moe_expert_matmul_backward_scratch_bytes(const moe_shape_t* shape, int32_t out_features,
+                                                int32_t act);
+
+/* Gradients of moe_expert_matmul (the residual's is grad_out itself):
+ *   grad_pre  = grad_out * act'(pre)                 bf16 [N,Wd]
+ *   grad_x    = grad_pre W_e                         bf16 [N,in_features]
+ *   grad_w[e] = sum over expert e's rows of grad_pre^T x   bf16 [E,Wd,in]
+ *   grad_bias[e] = sum over expert e's rows of grad_pre    fp32 [E,Wd]
+ * grad_x, grad_w and grad_bias may each be NULL (not computed); an expert
+ * without rows gets grad_w and grad_bias of zero; rows that hold no token are
+ * neither read into a sum nor written.  With act none, pre and grad_pre may
+ * be NULL and are not touched; otherwise both are needed (grad_pre is rounded
+ * to bf16, the operand type of the products; grad_bias sums the unrounded
+ * values).  scratch: device memory, 16-byte aligned, of the size above; only
+ * grad_bias needs it.  Sums are in a fixed order.  Errors as
+ * moe_expert_matmul. */
+moe_status_t moe_expert_matmul_backward(const moe_shape_t* shape, int32_t in_features,
+                                        int32_t out_features, int32_t act, const void* grad_out,
+                                        const void* x, const void* w, const void* pre,
+                                        const int32_t* counts, const int32_t* expert_off,
+                                        void* grad_pre, void* grad_x, void* grad_w,
+                                        float* grad_bias, void* scratch, size_t scratch_bytes,
+                                        void* ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Gradients of moe_combine's operands (those of shared and residual are
+ * grad_out itself; the gradient of moe_dispatch is moe_combine with gates of
+ * one):
+ *   grad_y[dst_pos[t,j],:] = bf16(gates[t,j] * grad_out[t,:])   bf16 [N,H]
+ *   grad_gates[t,j]        = <grad_out[t,:], y[dst_pos[t,j],:]> fp32 [T,k]
+ * A dropped slot (dst_pos < 0) gets grad_gates of 0; rows no slot maps to are
+ * not written.  A dst_pos value >= N sets MOE_ERR_DEVICE_RANGE and counts as
+ * dropped.  Sums are fp32 in a fixed order.  Buffers and alignment as
+ * moe_combine. */
+moe_status_t moe_combine_backward(const moe_shape_t* shape, const void* grad_out, const void* y,
+                                  const int32_t* dst_pos, const float* gates, void* grad_y,
+                                  float* grad_gates, void* ws, size_t ws_bytes,
+                                  moe_stream_t stream);
 
 /* moe_layout without a workspace, for callers that cannot allocate device
  * memory: plugin or custom-op hosts that give a kernel only its inputs and

@@ -1,0 +1,275 @@
+"""moe_route_scored and its gradient against the 64-bit definition: scores, groups, ties, masked and
+infinite logits, saturated scores, NaN rows, every size class; the gradient against the formulas and
+against differences.
+
+Ids are compared exactly: keys are those of binary64 arithmetic.  Gates: with renormalisation, or with
+sigmoid scores, they are quotients of binary64 scores rounded once to fp32 (2^-24, and 2^-40 for the
+binary64 steps); the full softmax's sum of up to 1024 exponentials is held to 1e-6, the tolerance of the
+library's other gates.
+"""
+import pytest
+import torch
+
+import expert_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+
+def _mod():
+    import combine_moe_route_07_b200 as m
+    return m
+
+
+def _gate_tol(func, renorm):
+    return 1e-6 if func == "softmax" and not renorm else 2.0 ** -24 + 2.0 ** -40
+
+
+def _run(logits, k, func, renorm, groups=1, top=1, gt=1, scale=1.0, bias=None, check=True):
+    m = _mod()
+    T, E = logits.shape
+    shape = m.MoeShape(tokens=T, hidden=8, experts=E, k=k, ranks=1, renorm=renorm)
+    ws = m.Workspace(shape)
+    rule = m.ScoreRule(func, groups, top, gt, scale)
+    ids, gates = m.moe_route_scored(shape, logits.cuda(), rule, None if bias is None else bias.cuda(), ws=ws)
+    if check:
+        m.moe_check(ws)
+    return ids.cpu(), gates.cpu(), ws
+
+
+def _compare(logits, k, func, renorm, groups=1, top=1, gt=1, scale=1.0, bias=None):
+    ids, gates, _ = _run(logits, k, func, renorm, groups, top, gt, scale, bias)
+    want, g, _ = ref.route(logits, k, func, renorm, groups, top, gt, scale, bias)
+    assert torch.equal(ids.long(), want)
+    tol = _gate_tol(func, renorm) * g.abs() + 2.0 ** -140  # gates below fp32's normal range
+    assert ((gates.double() - g).abs() <= tol).all()
+
+
+def _randn(*shape, seed=0, scale=1.0):
+    return torch.randn(*shape, generator=torch.Generator().manual_seed(seed)) * scale
+
+
+@pytest.mark.parametrize("func", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("T,E,k,groups,top,gt", [
+    (300, 8, 2, 1, 1, 1), (257, 64, 6, 8, 3, 2), (500, 256, 8, 8, 4, 2), (333, 512, 10, 8, 4, 2),
+    (129, 256, 8, 16, 3, 1), (65, 1024, 32, 1, 1, 1), (64, 1024, 16, 64, 5, 2), (77, 96, 5, 6, 2, 2),
+    (90, 100, 7, 4, 3, 1), (50, 33, 4, 1, 1, 1), (40, 160, 8, 10, 9, 2), (31, 5, 5, 5, 5, 1), (1, 256, 8, 8, 4, 2),
+    (12, 1, 1, 1, 1, 1), (200, 384, 8, 8, 4, 2), (200, 128, 8, 64, 8, 2), (100, 320, 6, 2, 1, 2),
+])
+def test_random(func, renorm, with_bias, T, E, k, groups, top, gt):
+    bias = _randn(E, seed=9, scale=0.05) if with_bias else None
+    _compare(_randn(T, E, seed=T + E, scale=1.5), k, func, renorm, groups, top, gt, 2.5, bias)
+
+
+@pytest.mark.parametrize("func", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("groups,top,gt", [(1, 1, 1), (8, 3, 2), (8, 4, 1)])
+def test_ties_take_the_lower_index(func, groups, top, gt):
+    E, k = 64, 6
+    g = torch.Generator().manual_seed(4)
+    rows = [torch.zeros(E), torch.ones(E) * -3.0]
+    rows += [torch.randint(0, n, (E,), generator=g).float() * 0.5 for n in (2, 3, 5, 9) for _ in range(40)]
+    rows.append(torch.tensor([0.0, -0.0] * (E // 2)))
+    _compare(torch.stack(rows), k, func, True, groups, top, gt)
+    # bias that makes different logits nearly, not exactly, equal keys
+    logits = _randn(200, E, seed=5)
+    s = ref.scores(logits, func)
+    _compare(logits, k, func, False, groups, top, gt, bias=(0.5 - s[0]).float())
+
+
+def test_neighbouring_keys_are_ordered_exactly():
+    """Logits one fp32 step apart around a common value: fp32 scores would tie."""
+    base = torch.tensor(0.75).view(torch.int32)
+    g = torch.Generator().manual_seed(6)
+    rows = [(base + torch.randperm(256, generator=g).int()).view(torch.float32) for _ in range(64)]
+    for func in ("softmax", "sigmoid"):
+        for groups, top, gt in ((1, 1, 1), (8, 4, 2)):
+            _compare(torch.stack(rows), 8, func, True, groups, top, gt)
+            _compare(torch.stack(rows), 8, func, True, groups, top, gt, bias=torch.full((256,), 0.125))
+
+
+def test_masked_and_saturated_logits():
+    E = 128
+    logits = _randn(300, E, seed=7, scale=2.0)
+    for t in range(300):  # all but t % 12 + 1 experts masked
+        logits[t, torch.randperm(E, generator=torch.Generator().manual_seed(t))[t % 12 + 1:]] = -float("inf")
+    for func in ("softmax", "sigmoid"):
+        _compare(logits, 6, func, True, 8, 4, 2)
+        _compare(logits, 6, func, False)
+    lowest = torch.where(torch.isinf(logits), torch.finfo(torch.float32).min, logits)
+    for func in ("softmax", "sigmoid"):
+        _compare(lowest, 6, func, True, 8, 4, 2)
+    # sigmoid of large logits is 1 in fp32 long before it is in binary64
+    _compare(_randn(100, E, seed=8, scale=30.0), 6, "sigmoid", True, 8, 4, 2)
+    _compare(_randn(100, E, seed=8, scale=300.0), 6, "softmax", True, 8, 4, 2)
+    _compare(_randn(100, E, seed=8, scale=1e-6), 6, "sigmoid", True, 8, 4, 2)
+    # nothing left: every sigmoid score is zero, gates are zero
+    ids, gates, _ = _run(torch.full((3, E), -float("inf")), 6, "sigmoid", True)
+    assert torch.equal(ids, torch.arange(6, dtype=torch.int32).expand(3, 6)) and (gates == 0).all()
+
+
+def test_bias_of_minus_infinity_excludes():
+    E = 64
+    logits, bias = _randn(100, E, seed=3), torch.zeros(E)
+    bias[torch.randperm(E, generator=torch.Generator().manual_seed(1))[:50]] = -float("inf")
+    for func in ("softmax", "sigmoid"):
+        _compare(logits, 8, func, True, bias=bias)
+        _compare(logits, 16, func, True, bias=bias)  # 14 experts left, then the lowest ids
+        _compare(logits, 8, func, True, 8, 2, 2, bias=bias)
+
+
+def test_nan_rows_are_reported_and_stay_valid():
+    m = _mod()
+    from combine_moe_route_07_b200 import _binding
+    for func, value in (("sigmoid", float("nan")), ("softmax", float("nan")), ("softmax", float("inf"))):
+        for E in (64, 256, 512):
+            logits = _randn(40, E, seed=2)
+            logits[17, E - 3] = value
+            ids, gates, ws = _run(logits, 4, func, True, check=False)
+            assert m.moe_get_device_error(ws) == (_binding.MOE_ERR_DEVICE_NAN, 17)
+            assert ids[17].tolist() == [0, 1, 2, 3] and (gates[17] == 0).all()
+            keep = [t for t in range(40) if t != 17]
+            want, g, _ = ref.route(logits[keep], 4, func, True)
+            assert torch.equal(ids[keep].long(), want)
+    ids, gates, ws = _run(torch.full((2, 64), -float("inf")), 4, "softmax", True, check=False)
+    assert m.moe_get_device_error(ws)[0] == _binding.MOE_ERR_DEVICE_NAN
+    ids, gates, ws = _run(_randn(2, 64), 4, "sigmoid", True, check=False,
+                          bias=torch.full((64,), float("inf")))
+    assert m.moe_get_device_error(ws)[0] == _binding.MOE_ERR_DEVICE_NAN
+
+
+def test_skewed_popularity_and_large_batch():
+    logits = _randn(20000, 512, seed=12) - 2.0 * torch.log(torch.arange(1, 513).float())
+    _compare(logits, 10, "sigmoid", True, 8, 4, 2, 2.5, _randn(512, seed=13, scale=0.05))
+    _compare(logits, 10, "softmax", True)
+    _compare(logits, 10, "softmax", False, bias=_randn(512, seed=13, scale=0.01))
+
+
+@pytest.mark.parametrize("func,renorm", [("softmax", True), ("softmax", False), ("sigmoid", True),
+                                         ("sigmoid", False)])
+@pytest.mark.parametrize("T,E,k", [(1, 1, 1), (3, 5, 2), (300, 64, 6), (257, 256, 8), (129, 515, 10),
+                                   (50, 1024, 32)])
+def test_gradient(func, renorm, T, E, k):
+    """fp32 steps: scores are off by at most 2^-20 relative, sums of k (or E) terms by (k or E) 2^-24, so
+    each part by 2^-19 + E 2^-24 of the magnitude of the terms it is a difference of.  The oracle goes
+    through the full softmax, whose two contributions to an expert outside the choice cancel only to
+    their 64-bit rounding: at most E + k steps of 2^-53 of the sum of the terms, below 2^-42 of it."""
+    m = _mod()
+    logits, up = _randn(T, E, seed=1, scale=1.5), _randn(T, k, seed=2)
+    ids, _, _ = ref.route(logits, k, func, renorm)
+    shape = m.MoeShape(tokens=T, hidden=8, experts=E, k=k, ranks=1, renorm=renorm)
+    ws = m.Workspace(shape)
+    got = m.moe_route_scored_backward(shape, logits.cuda(), m.ScoreRule(func, scale=2.5),
+                                      ids.int().cuda(), up.cuda(), ws=ws).cpu()
+    m.moe_check(ws)
+    z = logits.double().requires_grad_(True)
+    s = torch.sigmoid(z) if func == "sigmoid" else torch.softmax(z, 1)
+    gates = ref.gates_of(s, ids, renorm, 2.5)
+    want = torch.autograd.grad(gates, z, up.double())[0]
+    g = gates.detach().abs()
+    mag = torch.zeros(T, E, dtype=torch.float64).scatter_(1, ids, g * up.double().abs())
+    total = (g * up.double().abs()).sum(1, keepdim=True)
+    share = torch.zeros(T, E, dtype=torch.float64).scatter_(1, ids, torch.gather(s.detach(), 1, ids))
+    if renorm:
+        share = share / share.sum(1, keepdim=True)
+    elif func == "softmax":
+        share = s.detach()
+    mag = mag + share * total
+    assert ((got.double() - want).abs() <= (2.0 ** -19 + E * 2.0 ** -24) * mag + 2.0 ** -42 * total
+            + 2.0 ** -140).all()
+    if renorm or func == "sigmoid":
+        off = torch.ones(T, E, dtype=torch.bool).scatter_(1, ids, False)
+        assert (got[off] == 0).all()
+
+
+def test_gradient_agrees_with_differences():
+    m = _mod()
+    T, E, k = 4, 12, 3
+    logits, up = _randn(T, E, seed=1), _randn(T, k, seed=2)
+    for func in ("softmax", "sigmoid"):
+        for renorm in (False, True):
+            ids, _, _ = ref.route(logits, k, func, renorm)
+            shape = m.MoeShape(tokens=T, hidden=8, experts=E, k=k, ranks=1, renorm=renorm)
+            got = m.moe_route_scored_backward(shape, logits.cuda(), m.ScoreRule(func), ids.int().cuda(),
+                                              up.cuda(), ws=m.Workspace(shape)).cpu()
+            for e in range(E):
+                h = torch.zeros(E, dtype=torch.float64)
+                h[e] = 1e-5
+                f = [(ref.gates_of(ref.scores(logits.double() + q * h, func), ids, renorm, 1.0) * up).sum(1)
+                     for q in (1, -1)]
+                assert ((got[:, e].double() - (f[0] - f[1]) / 2e-5).abs() <= 1e-5).all()
+
+
+def test_gradient_edges():
+    m = _mod()
+    from combine_moe_route_07_b200 import _binding
+    T, E, k = 5, 40, 4
+    logits, up = _randn(T, E, seed=1), _randn(T, k, seed=2)
+    ids = torch.randint(0, E, (T, k), generator=torch.Generator().manual_seed(3), dtype=torch.int32)
+    ids[0] = torch.tensor([7, 3, 7, 7])  # one expert in three slots
+    ids[1] = torch.tensor([E, 2, 9, 11])  # outside
+    ids[2] = torch.tensor([5, -1, 6, 8])
+    shape = m.MoeShape(tokens=T, hidden=8, experts=E, k=k, ranks=1, renorm=False)
+    ws = m.Workspace(shape)
+    got = m.moe_route_scored_backward(shape, logits.cuda(), m.ScoreRule("sigmoid"), ids.cuda(), up.cuda(),
+                                      ws=ws).cpu()
+    assert m.moe_get_device_error(ws)[0] == _binding.MOE_ERR_DEVICE_RANGE
+    ok = (ids >= 0) & (ids < E)
+    s = torch.sigmoid(logits.double())
+    at = ids.clamp(0, E - 1).long()
+    part = torch.where(ok, up.double() * torch.gather(s * (1 - s), 1, at), 0.0)
+    want = torch.zeros(T, E, dtype=torch.float64).scatter_add_(1, at, part)
+    assert ((got.double() - want).abs() <= 2.0 ** -19 * up.double().abs().sum(1, keepdim=True)).all()
+    # saturated and masked: finite gradients, zero where the score is
+    logits = torch.full((2, E), -float("inf"))
+    logits[1] = 200.0
+    ids = torch.arange(k, dtype=torch.int32).expand(2, k).contiguous()
+    for renorm in (False, True):
+        shape = m.MoeShape(tokens=2, hidden=8, experts=E, k=k, ranks=1, renorm=renorm)
+        got = m.moe_route_scored_backward(shape, logits.cuda(), m.ScoreRule("sigmoid"), ids.cuda(),
+                                          up[:2].cuda(), ws=m.Workspace(shape)).cpu()
+        assert (got.abs() <= 2.0 ** -100).all()
+
+
+def test_unaligned_rows_and_other_stream():
+    """Logits and outputs that start 4 bytes behind a 16-byte boundary, on a stream of their own."""
+    m = _mod()
+    T, E, k = 70, 256, 8
+    base = _randn(T * E + 1, seed=1).cuda()
+    logits = base[1:].view(T, E)
+    shape = m.MoeShape(tokens=T, hidden=8, experts=E, k=k, ranks=1)
+    ws = m.Workspace(shape)
+    rule = m.ScoreRule("sigmoid", 8, 4, 2)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        ids, gates = m.moe_route_scored(shape, logits, rule, ws=ws)
+        grad = torch.full((T * E + 1,), 9.0, device="cuda")
+        m.moe_route_scored_backward(shape, logits, rule, ids, gates, ws=ws, grad_logits=grad[1:].view(T, E))
+    s.synchronize()
+    want, _, _ = ref.route(logits.cpu(), k, "sigmoid", True, 8, 4, 2)
+    assert torch.equal(ids.cpu().long(), want)
+    whole = m.moe_route_scored_backward(shape, logits.clone(), rule, ids, gates, ws=ws)
+    assert torch.equal(grad[1:].view(T, E), whole) and grad[0] == 9.0
+
+
+def test_no_tokens_and_wrong_arguments():
+    m = _mod()
+    shape = m.MoeShape(tokens=0, hidden=8, experts=8, k=2, ranks=1)
+    ws = m.Workspace(shape)
+    ids, gates = m.moe_route_scored(shape, torch.empty(0, 8, device="cuda"), m.ScoreRule(), ws=ws)
+    assert ids.shape == (0, 2) and gates.shape == (0, 2)
+    shape = m.MoeShape(tokens=4, hidden=8, experts=8, k=2, ranks=1)
+    logits = torch.zeros(4, 8, device="cuda")
+    for rule in (m.ScoreRule(groups=3), m.ScoreRule(groups=0), m.ScoreRule(groups=4, top_groups=5),
+                 m.ScoreRule(groups=8, top_groups=1), m.ScoreRule(group_top=3), m.ScoreRule(group_top=0),
+                 m.ScoreRule(groups=8, top_groups=4, group_top=2), m.ScoreRule(scale=0.0),
+                 m.ScoreRule(scale=float("nan"))):
+        with pytest.raises(m.MoeError):
+            m.moe_route_scored(shape, logits, rule, ws=ws)
+    with pytest.raises(ValueError):
+        m.moe_route_scored(shape, logits, m.ScoreRule("relu"), ws=ws)
+    with pytest.raises(ValueError):
+        m.moe_route_scored(shape, logits.cpu(), m.ScoreRule(), ws=ws)
+    with pytest.raises(ValueError):
+        m.moe_route_scored(shape, logits.t().contiguous().t(), m.ScoreRule(), ws=ws)
