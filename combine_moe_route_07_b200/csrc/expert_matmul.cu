@@ -24,6 +24,7 @@
 // shares its operands, so a 256 x 256 tile costs each SM 32 KiB of copies per
 // 64-deep slice; one CTA alone moves 48 KiB for the same work and is bound by
 // the L2 (about 10 TB/s).  Every wait is bounded.
+#include <limits.h>
 #include <math.h>
 
 #include "block_scan.cuh"
@@ -37,14 +38,13 @@ namespace {
 
 constexpr int kBK = 64;       // contraction depth of a stage
 constexpr int kBM = 128;      // rows of the M operand on each CTA of a pair
-constexpr int kBN = 256;      // columns of a tile
-constexpr int kBox = 32;      // token rows of one copy
+constexpr int kBN = 256;      // columns of one accumulator
 constexpr int kABytes = kBM * kBK * 2;
-constexpr int kStages = 6;
-constexpr int kStageBytes = 32 * 1024;
+constexpr int kSlots = 8;     // slices in flight, at most (a power of two)
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = (4 + kEpiWarps) * 32;
-constexpr int kEpiBytes = kEpiWarps * 2048;  // 32 x 32 bf16 a warp
+constexpr int kEpiBytes = kEpiWarps * 2 * 2048;  // two 32 x 32 bf16 blocks a warp
+constexpr int kMaxSlice = kABytes + 2 * 128 * kBK * 2;
 constexpr int kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -52,7 +52,9 @@ enum { kFwd = 0, kRows = 1, kWeights = 2 };
 
 struct GemmParams {
   CUtensorMap ma;  // M operand: weights [E][W][K]; weights gradient: dz [N][W]
-  CUtensorMap mb;  // N operand: x or dz [N][..]
+  CUtensorMap mb[3];  // N operand, x or dz [N][..], in boxes of 32, 64 and 128 rows
+                      // (weights gradient: one of 64)
+  CUtensorMap mo, mp;  // out and pre, in boxes of 32 x 32
   const int32_t* counts;  // NULL: one expert holding every row
   const int32_t* off;
   const float* bias;
@@ -67,6 +69,8 @@ struct GemmParams {
   int kdim;    // contraction length (weights gradient: per expert)
   int cols;    // weights gradient: columns of x
   int band;    // token tiles an expert walks together
+  int max_n;   // columns of a tile, at most (256 or 512)
+  int ring;    // bytes of the operand ring
   int act;
 };
 
@@ -123,10 +127,16 @@ __device__ __forceinline__ uint16_t to_bf16(float v) {
   return r;
 }
 
-// Tile t of the forward / rows products.
+// A tile: its expert, channel tile, first row (weights gradient: column) and
+// rows; one or two accumulators ("parts") of `n` columns each.
 struct Tile {
-  int e, c, row0, rows;  // expert, channel tile, first row, rows
+  int e, c, row0, rows, parts, n;
 };
+
+// Token rows that copies bring for `half` (a multiple of 16, up to 128) wanted:
+// one box of 32, 64 or 128, or 64 + 32.  Few large copies: with boxes of 32
+// rows alone a 256-column tile ran at 1230 TFLOP/s, with one of 128 at 1340.
+__device__ __forceinline__ int box_rows(int half) { return (half + 31) & ~31; }
 
 template <int MODE, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
@@ -134,10 +144,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   constexpr int kTileM = GATED ? kBM : 2 * kBM;  // output channels of a pair's tile
   extern __shared__ uint8_t smem_raw[];
   // tempty and fixed are waited on by the even CTA only; full too, but for an odd
-  // CTA's slices with stale rows.  A stage's barriers see at most one phase at a
-  // time: the stage is filled again only once the instructions that read it are done.
-  __shared__ uint64_t full[kStages], empty[kStages], tfull[2], tempty[2], drain;
-  __shared__ uint64_t fixed[kStages];  // weights gradient: the odd CTA's stale rows are zero
+  // CTA's slices with stale rows.  A slot's barriers see at most one phase at a
+  // time: the slot is used again only once the instructions that read it are done.
+  __shared__ uint64_t full[kSlots], empty[kSlots], tfull[2], tempty[2], drain;
+  __shared__ uint64_t fixed[kSlots];  // weights gradient: the odd CTA's stale rows are zero
   __shared__ uint64_t swap[4];      // gated: between the two warps of a channel block
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
@@ -145,8 +155,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   __shared__ int32_t warp_tot[kGemmThreads / 32];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* epi = smem + kStages * kStageBytes;
-  int32_t* seg_off = reinterpret_cast<int32_t*>(smem + kStages * kStageBytes + kEpiBytes);
+  uint8_t* epi = smem + P.ring;
+  int32_t* seg_off = reinterpret_cast<int32_t*>(epi + kEpiBytes);
   int32_t* seg_rows = seg_off + P.E;
   int32_t* first = seg_rows + P.E;  // forward / rows: exclusive prefix of token tiles [E+1]
 
@@ -154,7 +164,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   const uint32_t rank = cluster_rank();
   const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
   if (tid == 0) {
-    for (int s = 0; s < kStages; ++s) {
+    for (int s = 0; s < kSlots; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
       mbar_init(&fixed[s], 1);
@@ -169,7 +179,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     rows_sum = 0ull;
     mbar_fence_init();
     tma_prefetch_map(&P.ma);
-    tma_prefetch_map(&P.mb);
+    tma_prefetch_map(&P.mb[0]);
   }
   if (wid == 1) tmem_alloc(&tmem_slot, kTmemCols);
   __syncthreads();
@@ -181,7 +191,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     seg_off[e] = s.off;
     seg_rows[e] = s.rows;
     my_rows += (unsigned long long)s.rows;
-    if (MODE != kWeights) first[e] = (s.rows + kBN - 1) / kBN;
+    if (MODE != kWeights) first[e] = (s.rows + P.max_n - 1) / P.max_n;
   }
   if (my_rows != 0ull) atomicAdd(&rows_sum, my_rows);
   tc_fence_before();
@@ -209,11 +219,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   volatile int* stop = &abort_flag;
   // Wait for a phase; false: it gave up, or another role did.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    if (mbar_try_wait_cluster(bar, parity)) return true;
-    const uint64_t t0 = global_ns();
-    for (unsigned it = 0; it < (1u << 24); ++it) {
+    uint64_t t0 = 0;  // the clock is read only by waits that take long: it is slow
+    for (unsigned it = 1; it < (1u << 24); ++it) {
       if (mbar_try_wait_cluster(bar, parity)) return true;
-      if ((it & 63u) == 63u && (*stop != 0 || global_ns() - t0 > kWaitNs)) break;
+      if ((it & 63u) == 0u) {
+        const uint64_t now = global_ns();
+        if (t0 == 0) t0 = now;
+        if (*stop != 0 || now - t0 > kWaitNs) break;
+      }
     }
     if (*stop == 0) report(P.hdr, MOE_ERR_DEVICE_TIMEOUT, blockIdx.x);
     *stop = 1;
@@ -235,6 +248,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       r.c = u / nt;
       r.row0 = (u - r.c * nt) * kBN;  // first column
       r.rows = min(kBN, P.cols - r.row0);
+      r.parts = 1;
+      r.n = (r.rows + 31) & ~31;
     } else {
       const int u = t / ctiles;
       int lo = 0, hi = P.E;  // first[lo] <= u < first[hi]
@@ -257,8 +272,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       r.c = v / nb;
       r.row0 = n * per;
       r.rows = min(per, seg_rows[lo] - r.row0);
+      r.parts = r.rows > kBN ? 2 : 1;
+      r.n = r.parts == 2 ? ((r.rows + 1) / 2 + 31) & ~31 : (r.rows + 31) & ~31;
     }
     return r;
+  };
+  // The ring: a slice of a tile takes the bytes it needs (the M operand's 16 KiB and
+  // the rows of the N operand), behind the one before it or, where it does not fit
+  // there, at the ring's start.  Every role places the slices alike.
+  auto slice_bytes = [&](const Tile& r) -> int {
+    return kABytes + (MODE == kWeights ? ((r.n / 2 + 63) >> 6) * 8192
+                                       : r.parts * box_rows(r.n / 2) * (kBK * 2));
+  };
+  auto place = [&](int& head, int bytes) -> int {
+    if (head + bytes > P.ring) head = 0;
+    const int at = head;
+    head += bytes;
+    return at;
   };
   // Rows of the last slice that belong to the expert, when fewer than its
   // 16-deep steps take in (weights gradient).
@@ -281,60 +311,88 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   if (wid == 0) {
     // ---- producer -------------------------------------------------------------
     if (lane == 0) {
-      uint32_t it = 0;
+      uint32_t it = 0, old = 0;  // slices issued, and those known to be used up
+      int head = 0, room = P.ring >> 10;
+      uint64_t taken = 0;  // byte s: KiB that slot s's slice took, the gap before it too
+      const uint32_t even_full = even_addr(&full[0]);
       bool ok = true;
       for (int t = pair; t < total && ok; t += pairs) {
         const Tile r = tile_of(t);
         const int depth = MODE == kWeights ? seg_rows[r.e] : P.kdim;
         const int nkb = (depth + kBK - 1) / kBK;
-        const int half = ((r.rows + 31) & ~31) / 2;  // columns of D from each CTA's operand
-        const int boxes = MODE == kWeights ? (half + 63) >> 6 : (half + kBox - 1) / kBox;
-        const uint32_t bytes = (uint32_t)kABytes + (uint32_t)boxes * (MODE == kWeights ? 8192u : kBox * 128u);
+        const int half = r.n / 2;  // columns of an accumulator from each CTA's operand
+        const int bytes = slice_bytes(r);
         const int row = seg_off[r.e] + (MODE == kWeights ? 0 : r.row0 + (int)rank * half);
-        const int col = r.row0 + (int)rank * half;                     // weights gradient
+        const int col = r.row0 + (int)rank * half;  // weights gradient
         const int ch = r.c * kTileM + (int)rank * (GATED ? kBM / 2 : kBM);
         for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int s = it % kStages;
-          if (!wait(&empty[s], ((it / kStages) & 1u) ^ 1u)) {
-            ok = false;
-            break;
+          const int s = it % kSlots;
+          const int gap = head + bytes > P.ring ? P.ring - head : 0;
+          const int at = place(head, bytes);
+          const int need = (bytes + gap) >> 10;
+          // the oldest slices make room: for the bytes, and for the slot
+          while (room < need || it - old == kSlots) {
+            const int o = old % kSlots;
+            if (!wait(&empty[o], (old / kSlots) & 1u)) {
+              ok = false;
+              break;
+            }
+            room += (int)((taken >> (8 * o)) & 255u);
+            ++old;
           }
-          uint8_t* a = smem + s * kStageBytes;
+          if (!ok) break;
+          room -= need;
+          taken = (taken & ~(255ull << (8 * s))) | ((uint64_t)need << (8 * s));
+          uint8_t* a = smem + at;
           uint8_t* b = a + kABytes;
           // both CTAs' copies complete on the even CTA's barrier, except that an odd CTA's
           // slice with stale rows passes through that CTA's hands first
-          uint32_t bar = even_addr(&full[s]);
+          uint32_t bar = even_full + s * 8;
           const bool apart = stale_tail(depth, kb);
           if (rank == 0) {
-            mbar_arrive_expect_tx(&full[s], apart ? bytes : 2u * bytes);
+            mbar_arrive_expect_tx(&full[s], (uint32_t)(apart ? bytes : 2 * bytes));
           } else if (apart) {
-            mbar_arrive_expect_tx(&full[s], bytes);
+            mbar_arrive_expect_tx(&full[s], (uint32_t)bytes);
             bar = smem_addr(&full[s]);
           }
-          if constexpr (MODE == kFwd) {
-            tma_load_3d(a, &P.ma, kb * kBK, ch, r.e, bar);
-            if constexpr (GATED) tma_load_3d(a + kABytes / 2, &P.ma, kb * kBK, P.M + ch, r.e, bar);
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(b + i * kBox * 128, &P.mb, kb * kBK, row + i * kBox, bar);
-          } else if constexpr (MODE == kRows) {
-            tma_load_3d(a, &P.ma, ch, kb * kBK, r.e, bar);
-            tma_load_3d(a + 8192, &P.ma, ch + 64, kb * kBK, r.e, bar);
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(b + i * kBox * 128, &P.mb, kb * kBK, row + i * kBox, bar);
-          } else {
+          if constexpr (MODE == kWeights) {
             tma_load_2d(a, &P.ma, ch, row + kb * kBK, bar);
             tma_load_2d(a + 8192, &P.ma, ch + 64, row + kb * kBK, bar);
-            for (int i = 0; i < boxes; ++i)
-              tma_load_2d(b + i * 8192, &P.mb, col + i * 64, row + kb * kBK, bar);
+            tma_load_2d(b, &P.mb[0], col, row + kb * kBK, bar);
+            if (half > 64) tma_load_2d(b + 8192, &P.mb[0], col + 64, row + kb * kBK, bar);
+          } else {
+            if constexpr (MODE == kFwd) {
+              tma_load_3d(a, &P.ma, kb * kBK, ch, r.e, bar);
+              if constexpr (GATED)
+                tma_load_3d(a + kABytes / 2, &P.ma, kb * kBK, P.M + ch, r.e, bar);
+            } else {
+              tma_load_3d(a, &P.ma, ch, kb * kBK, r.e, bar);
+              tma_load_3d(a + 8192, &P.ma, ch + 64, kb * kBK, r.e, bar);
+            }
+            const int fetched = box_rows(half);
+            for (int p = 0; p < r.parts; ++p) {
+              uint8_t* bp = b + p * fetched * (kBK * 2);
+              const int y = row + p * r.n;
+              if (fetched == 128) {
+                tma_load_2d(bp, &P.mb[2], kb * kBK, y, bar);
+              } else {
+                int done = 0;
+                if (fetched >= 64) {
+                  tma_load_2d(bp, &P.mb[1], kb * kBK, y, bar);
+                  done = 64;
+                }
+                if (fetched > done) tma_load_2d(bp + done * (kBK * 2), &P.mb[0], kb * kBK, y + done, bar);
+              }
+            }
           }
         }
       }
       if (!ok) {  // copies in flight land before the pair ends
         if (rank == 0)
-          for (uint32_t j = it > kStages ? it - kStages : 0; j < it; ++j)
-            mbar_wait_bounded(&full[j % kStages], (j / kStages) & 1u, 1000000ull);
+          for (uint32_t j = old; j < it; ++j)
+            mbar_wait_bounded(&full[j % kSlots], (j / kSlots) & 1u, 1000000ull);
         else
-          mbar_wait_bounded(&drain, 1u ^ 1u, 1000000ull);  // a pause; nothing arrives
+          mbar_wait_bounded(&drain, 0u, 1000000ull);  // a pause
       }
     }
     __syncwarp();
@@ -342,30 +400,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     // ---- matrix instructions ----------------------------------------------------
     constexpr uint32_t a_mn = MODE == kFwd ? 0u : 1u, b_mn = MODE == kWeights ? 1u : 0u;
     uint32_t it = 0, nacc = 0, fix_par = 0;  // bit s: parity of fixed[s]'s next phase
+    int head = 0;
     bool ok = true;
     for (int t = pair; t < total && ok; t += pairs) {
       const Tile r = tile_of(t);
       const int depth = MODE == kWeights ? seg_rows[r.e] : P.kdim;
       const int nkb = (depth + kBK - 1) / kBK;
       if (nkb == 0) continue;
-      const uint32_t acc = nacc & 1u;
-      if (!warp_wait(&tempty[acc], ((nacc >> 1) & 1u) ^ 1u)) break;
+      for (int p = 0; p < r.parts && ok; ++p)
+        ok = warp_wait(&tempty[(nacc + p) & 1u], (((nacc + p) >> 1) & 1u) ^ 1u);
+      if (!ok) break;
       tc_fence_after();
-      ++nacc;
-      const uint32_t d = tmem + acc * 256u;
-      const int n = (r.rows + 31) & ~31;
-      const uint32_t idesc = umma_idesc(2 * kBM, (uint32_t)n, a_mn, b_mn);
+      const uint32_t idesc = umma_idesc(2 * kBM, (uint32_t)r.n, a_mn, b_mn);
+      const int bytes = slice_bytes(r);
+      const uint32_t part_bytes = (uint32_t)((bytes - kABytes) / r.parts);
       for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const int s = it % kStages;
-        if (!warp_wait(&full[s], (it / kStages) & 1u)) {
+        const int s = it % kSlots;
+        const int at = place(head, bytes);
+        if (!warp_wait(&full[s], (it / kSlots) & 1u)) {
           ok = false;
           break;
         }
-        uint8_t* a = smem + s * kStageBytes;
         int ksteps = kBK / 16;
         if constexpr (MODE == kWeights) ksteps = (min(kBK, depth - kb * kBK) + 15) >> 4;
         if (stale_tail(depth, kb)) {
-          zero_stale(a, depth, kb, 2 + ((n / 2 + 63) >> 6));
+          zero_stale(smem + at, depth, kb, bytes / 8192);
           if (!warp_wait(&fixed[s], (fix_par >> s) & 1u)) {
             ok = false;
             break;
@@ -374,19 +433,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         }
         tc_fence_after();
         if (lane == 0) {
-          const uint32_t sa = smem_addr(a), sb = sa + kABytes;
-          for (int q = 0; q < ksteps; ++q) {
-            const uint64_t da = a_mn ? umma_desc(sa + q * 2048, 8192, 1024)
-                                     : umma_desc(sa + q * 32, 16, 1024);
-            const uint64_t db = b_mn ? umma_desc(sb + q * 2048, 8192, 1024)
-                                     : umma_desc(sb + q * 32, 16, 1024);
-            umma_f16(d, da, db, idesc, kb > 0 || q > 0);
+          const uint32_t sa = smem_addr(smem + at), sb = sa + kABytes;
+          const uint64_t da = a_mn ? umma_desc(sa, 8192, 1024) : umma_desc(sa, 16, 1024);
+          const uint64_t db = b_mn ? umma_desc(sb, 8192, 1024) : umma_desc(sb, 16, 1024);
+          // a 16-deep step further: 32 bytes along K-major rows, 2048 over MN-major ones
+          constexpr uint64_t sa16 = a_mn ? 128 : 2, sb16 = b_mn ? 128 : 2;
+          const uint32_t d0 = tmem + (nacc & 1u) * 256u;
+#pragma unroll
+          for (int q = 0; q < kBK / 16; ++q)
+            if (MODE != kWeights || q < ksteps)
+              umma_f16(d0, da + q * sa16, db + q * sb16, idesc, kb > 0 || q > 0);
+          if (r.parts == 2) {
+            const uint64_t db1 = db + (part_bytes >> 4);
+            const uint32_t d1 = tmem + (~nacc & 1u) * 256u;
+#pragma unroll
+            for (int q = 0; q < kBK / 16; ++q)
+              umma_f16(d1, da + q * sa16, db1 + q * sb16, idesc, kb > 0 || q > 0);
           }
           umma_commit(&empty[s]);
         }
         __syncwarp();
       }
-      if (ok && lane == 0) umma_commit(&tfull[acc]);
+      if (!ok) break;
+      for (int p = 0; p < r.parts; ++p, ++nacc)
+        if (lane == 0) umma_commit(&tfull[nacc & 1u]);
       __syncwarp();
     }
     if (*stop != 0) {
@@ -399,108 +469,164 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   } else if (wid == 1 && MODE == kWeights) {
     // ---- odd CTA: its stale rows ------------------------------------------------
     uint32_t it = 0, par = 0;  // bit s: parity of full[s]'s next phase here
+    int head = 0;
     for (int t = pair; t < total; t += pairs) {
       const Tile r = tile_of(t);
       const int depth = seg_rows[r.e];
       const int nkb = (depth + kBK - 1) / kBK;
       if (nkb == 0) continue;
+      const int bytes = slice_bytes(r);
+      for (int kb = 0; kb < nkb - 1; ++kb) place(head, bytes);
+      const int at = place(head, bytes);
+      it += nkb;
       if (stale_tail(depth, nkb - 1)) {
-        const int n = (r.rows + 31) & ~31;
-        const int s = (int)((it + nkb - 1) % kStages);
+        const int s = (int)((it - 1) % kSlots);
         if (!warp_wait(&full[s], (par >> s) & 1u)) break;
         par ^= 1u << s;
-        zero_stale(smem + s * kStageBytes, depth, nkb - 1, 2 + ((n / 2 + 63) >> 6));
+        zero_stale(smem + at, depth, nkb - 1, bytes / 8192);
         if (lane == 0) mbar_arrive_cluster(even_addr(&fixed[s]));
       }
-      it += nkb;
     }
   } else if (wid >= 4) {
     // ---- epilogue ---------------------------------------------------------------
-    // Warps 4..7 and 8..11: quarter q (rows 32q..32q+31) of the accumulator, in
-    // turn every second block of 32 columns.  A block is staged in the warp's
-    // 2 KiB as 32 rows of 64 bytes, 16-byte pieces swizzled by the row, so that
-    // both the column-wise and the row-wise accesses are free of conflicts.
+    // Warps 4..7 and 8..11: quarter q (rows 32q..32q+31) of an accumulator, in
+    // turn every second block of 32 columns.  A block is staged as 32 rows of 64
+    // bytes, 16-byte pieces swizzled by the row (the tensor map's 64-byte swizzle:
+    // neither the column-wise nor the row-wise accesses conflict), and stored by a
+    // tensor-map copy that runs while the warp goes on with its other staging
+    // block.  Blocks that end inside (rows behind them belong to another expert,
+    // or to nobody) are stored by the lanes.
     const int q = wid & 3, half = (wid - 4) >> 2;
-    uint8_t* buf = epi + (wid - 4) * 2048;
-    uint16_t* buf16 = reinterpret_cast<uint16_t*>(buf);
+    uint8_t* const blocks = epi + (wid - 4) * 4096;
     const int frow = lane >> 2, fcol = (lane & 3) * 8;
-    // piece (row, lane & 3) of the staged block
-    auto piece = [&](int row) {
+    uint32_t uses = 0;
+    // A staging block.  Every use is one bulk group, empty or not: with at most one
+    // group still reading, the use before last is done.
+    auto open_block = [&]() -> uint8_t* {
+      if (lane == 0) bulk_wait_read<1>();
+      __syncwarp();
+      return blocks + (uses++ & 1u) * 2048;
+    };
+    // piece (row, lane & 3) of a staged block
+    auto piece = [&](uint8_t* buf, int row) {
       return reinterpret_cast<uint4*>(buf + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
     };
     // this lane's column of a staged row
-    auto cell = [&](int row) {
-      return buf16 + row * 32 + (((lane >> 3) ^ ((row >> 1) & 3)) << 3) + (lane & 7);
+    auto cell = [&](uint8_t* buf, int row) {
+      return reinterpret_cast<uint16_t*>(buf) + row * 32 +
+             (((lane >> 3) ^ ((row >> 1) & 3)) << 3) + (lane & 7);
     };
-    // the first 8 * n8 staged rows -> rows of `dst`, `stride` elements apart, 64
-    // bytes each (widths are multiples of 8 elements)
-    auto flush = [&](uint16_t* dst, size_t stride, int nrows, int ncols, int n8) {
-      __syncwarp();
+    // Token-major block of `box` rows at (row, ch) of a matrix `stride` wide, of which
+    // `nrows` rows and `ncols` columns (a multiple of 8) are this expert's.
+    auto close_tokens = [&](uint8_t* buf, const CUtensorMap* map, uint16_t* base, int64_t row,
+                            int ch, int stride, int box, int nrows, int ncols) {
+      if (nrows >= box) {
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          if (ncols > 0) tma_store_2d(map, buf, ch, (int)row);
+          bulk_commit();
+        }
+      } else {
+        __syncwarp();
+        uint16_t* dst = base + (size_t)row * stride + ch;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int rr = i * 8 + frow;
-        if (i < n8 && rr < nrows && fcol < ncols) st16(dst + (size_t)rr * stride + fcol, *piece(rr));
+        for (int i = 0; i < 4; ++i) {
+          const int rr = i * 8 + frow;
+          if (rr < nrows && fcol < ncols) st16(dst + (size_t)rr * stride + fcol, *piece(buf, rr));
+        }
+        __syncwarp();
+        if (lane == 0) bulk_commit();
       }
-      __syncwarp();
     };
     uint32_t nacc = 0, nswap = 0;
     bool ok = true;
     for (int t = pair; t < total && ok; t += pairs) {
       const Tile r = tile_of(t);
       const bool empty_sum = MODE == kWeights && seg_rows[r.e] == 0;
-      const uint32_t acc = nacc & 1u;
-      if (!empty_sum) {
-        if (!warp_wait(&tfull[acc], (nacc >> 1) & 1u)) break;
-        tc_fence_after();
-        ++nacc;
-      }
-      const uint32_t d = tmem + acc * 256u + ((uint32_t)(q * 32) << 16);
       // this warp's first channel (gated: of the half that it holds)
       const int ch0 = GATED ? r.c * kTileM + (int)rank * 64 + (q & 1) * 32
                             : r.c * kTileM + (int)rank * kBM + q * 32;
       const int nc = P.M - ch0;
-      const int nchunks = (r.rows + 31) >> 5;
-      if constexpr (MODE == kWeights) {
-        uint16_t* dst = P.out + ((size_t)r.e * P.M + ch0) * P.cols + r.row0;
-        for (int j = half; j < nchunks; j += 2) {
-          uint32_t v[32];
-          if (!empty_sum) {
-            tmem_ld32(d + j * 32, v);
-            tmem_ld_wait();
-          } else {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) v[i] = 0u;
+      for (int p = 0; p < r.parts && ok; ++p) {
+        const uint32_t acc = nacc & 1u;
+        if (!empty_sum) {
+          if (!warp_wait(&tfull[acc], (nacc >> 1) & 1u)) {
+            ok = false;
+            break;
           }
-          // this lane holds 32 columns of one row of dW
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t p[4];
-#pragma unroll
-            for (int u = 0; u < 4; ++u)
-              p[u] = pack2(__uint_as_float(v[8 * i + 2 * u]), __uint_as_float(v[8 * i + 2 * u + 1]));
-            *reinterpret_cast<uint4*>(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-                make_uint4(p[0], p[1], p[2], p[3]);
-          }
-          flush(dst + j * 32, (size_t)P.cols, nc, r.rows - j * 32, 4);
+          tc_fence_after();
+          ++nacc;
         }
-      } else {
-        const int ch = ch0 + lane;
-        const bool up_half = GATED && q >= 2;
-        float b0 = 0.0f;
-        if constexpr (MODE == kFwd) {
+        const uint32_t d = tmem + acc * 256u + ((uint32_t)(q * 32) << 16);
+        const int row0 = r.row0 + p * r.n;
+        const int rows = min(r.n, r.row0 + r.rows - row0);
+        const int nchunks = (rows + 31) >> 5;
+        if constexpr (MODE == kWeights) {
+          // this lane holds 32 columns of one row of dW; two blocks at a time
+          auto stage = [&](const uint32_t(&v)[32], int j) {
+            uint8_t* buf = open_block();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t w[4];
+#pragma unroll
+              for (int u = 0; u < 4; ++u)
+                w[u] = pack2(__uint_as_float(v[8 * i + 2 * u]), __uint_as_float(v[8 * i + 2 * u + 1]));
+              *reinterpret_cast<uint4*>(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
+                  make_uint4(w[0], w[1], w[2], w[3]);
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+              if (nc > 0) tma_store_3d(&P.mo, buf, row0 + j * 32, ch0, r.e);
+              bulk_commit();
+            }
+          };
+          for (int j = half; j < nchunks; j += 4) {
+            uint32_t v0[32], v1[32];
+            if (!empty_sum) {
+              tmem_ld32(d + j * 32, v0);
+              if (j + 2 < nchunks) tmem_ld32(d + j * 32 + 64, v1);
+              tmem_ld_wait();
+            } else {
+#pragma unroll
+              for (int i = 0; i < 32; ++i) v0[i] = v1[i] = 0u;
+            }
+            stage(v0, j);
+            if (j + 2 < nchunks) stage(v1, j + 2);
+          }
+        } else if constexpr (MODE == kRows) {
+          // this lane holds one channel of 32 tokens: staged token-major
+          const int64_t row = (int64_t)seg_off[r.e] + row0;
+          auto stage = [&](const uint32_t(&v)[32], int j) {
+            uint8_t* buf = open_block();
+#pragma unroll
+            for (int i = 0; i < 32; ++i) *cell(buf, i) = to_bf16(__uint_as_float(v[i]));
+            close_tokens(buf, &P.mo, P.out, row + j * 32, ch0, P.M, 32, rows - j * 32, nc);
+          };
+          for (int j = half; j < nchunks; j += 4) {
+            uint32_t v0[32], v1[32];
+            tmem_ld32(d + j * 32, v0);
+            if (j + 2 < nchunks) tmem_ld32(d + j * 32 + 64, v1);
+            tmem_ld_wait();
+            stage(v0, j);
+            if (j + 2 < nchunks) stage(v1, j + 2);
+          }
+        } else {
+          const int ch = ch0 + lane;
+          const bool up_half = GATED && q >= 2;
+          float b0 = 0.0f;
           if (P.bias != nullptr && ch < P.M)
             b0 = __ldg(P.bias + (size_t)r.e * P.M * (GATED ? 2 : 1) + (up_half ? P.M : 0) + ch);
-        }
-        const int64_t row = (int64_t)seg_off[r.e] + r.row0;
-        for (int j = half; j < nchunks; j += 2) {
-          const int64_t row_j = row + j * 32;
-          const int nr = r.rows - j * 32;
-          // tokens whose results this warp writes: all 32, or gated its half
-          const int tok0 = up_half ? 16 : 0;
-          constexpr int kTok = GATED ? 16 : 32;
-          // the residual's block, on its way while the accumulator is read
-          uint4 res[MODE == kFwd ? kTok / 8 : 1];
-          if constexpr (MODE == kFwd) {
+          const int64_t row = (int64_t)seg_off[r.e] + row0;
+          for (int j = half; j < nchunks; j += 2) {
+            const int64_t row_j = row + j * 32;
+            const int nr = rows - j * 32;
+            // tokens whose results this warp writes: all 32, or gated its half
+            const int tok0 = up_half ? 16 : 0;
+            constexpr int kTok = GATED ? 16 : 32;
+            // the residual's block, on its way while the accumulator is read
+            uint4 res[kTok / 8];
             if (P.residual != nullptr) {
               const uint16_t* src = P.residual + (row_j + tok0) * P.M + ch0;
 #pragma unroll
@@ -511,53 +637,58 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                              : make_uint4(0, 0, 0, 0);
               }
             }
-          }
-          uint32_t v[32];
-          tmem_ld32(d + j * 32, v);
-          tmem_ld_wait();
-          // this lane holds one channel of 32 tokens: staged token-major
-          float z[32];
+            uint32_t v[32];
+            tmem_ld32(d + j * 32, v);
+            tmem_ld_wait();
+            // this lane holds one channel of 32 tokens: staged token-major
+            float z[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(v[i]) + b0;
-          if constexpr (MODE == kFwd) {
+            for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(v[i]) + b0;
             if (P.pre != nullptr) {
-              const size_t wide = (size_t)P.M * (GATED ? 2 : 1);
+              const int wide = P.M * (GATED ? 2 : 1);
+              uint8_t* buf = open_block();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) *cell(i) = to_bf16(z[i]);
-              flush(P.pre + row_j * wide + (up_half ? P.M : 0) + ch0, wide, nr, nc, 4);
+              for (int i = 0; i < 32; ++i) *cell(buf, i) = to_bf16(z[i]);
+              // (a gate half's block may reach into the up half's columns: lane stores)
+              const bool inside = !GATED || up_half || nc >= 32;
+              close_tokens(buf, &P.mp, P.pre, row_j, (up_half ? P.M : 0) + ch0, wide,
+                           inside ? 32 : INT_MAX, nr, nc);
             }
-          }
-          if constexpr (GATED) {
-            // lanes 0..63 of the accumulator are gates, 64..127 the same channels' ups.
-            // The gate's warp takes tokens 0..15, the up's 16..31: each hands the other
-            // its 16 values through its staging block, in fp32.
-            uint64_t* bar = &swap[half * 2 + (q & 1)];
-            float* mine = reinterpret_cast<float*>(buf);
-            const float* theirs = reinterpret_cast<const float*>(epi + ((wid - 4) ^ 2) * 2048);
+            if constexpr (GATED) {
+              // lanes 0..63 of the accumulator are gates, 64..127 the same channels' ups.
+              // The gate's warp takes tokens 0..15, the up's 16..31: each hands the other
+              // its 16 values through a staging block, in fp32.
+              uint64_t* bar = &swap[half * 2 + (q & 1)];
+              uint8_t* buf = open_block();
+              float* mine = reinterpret_cast<float*>(buf);
+              const float* theirs =
+                  reinterpret_cast<const float*>(epi + ((wid - 4) ^ 2) * 4096 + (buf - blocks));
 #pragma unroll
-            for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = up_half ? z[i] : z[16 + i];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
-            if (!warp_wait(bar, nswap++ & 1u)) {
-              ok = false;
-              break;
-            }
-            float other[16];
+              for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = up_half ? z[i] : z[16 + i];
+              __syncwarp();
+              if (lane == 0) {
+                bulk_commit();
+                mbar_arrive(bar);
+              }
+              if (!warp_wait(bar, nswap++ & 1u)) {
+                ok = false;
+                break;
+              }
+              float other[16];
 #pragma unroll
-            for (int i = 0; i < 16; ++i) other[i] = theirs[i * 32 + lane];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(bar);
-            if (!warp_wait(bar, nswap++ & 1u)) {
-              ok = false;
-              break;
-            }
+              for (int i = 0; i < 16; ++i) other[i] = theirs[i * 32 + lane];
+              __syncwarp();
+              if (lane == 0) mbar_arrive(bar);
+              if (!warp_wait(bar, nswap++ & 1u)) {
+                ok = false;
+                break;
+              }
 #pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              const float g = up_half ? other[i] : z[i], u = up_half ? z[16 + i] : other[i];
-              z[i] = g * sigmoid_f(g) * u;
-            }
-          } else if constexpr (MODE == kFwd) {
-            if (P.act == MOE_ACT_RELU) {
+              for (int i = 0; i < 16; ++i) {
+                const float g = up_half ? other[i] : z[i], u = up_half ? z[16 + i] : other[i];
+                z[i] = g * sigmoid_f(g) * u;
+              }
+            } else if (P.act == MOE_ACT_RELU) {
 #pragma unroll
               for (int i = 0; i < 32; ++i) z[i] = z[i] < 0.0f ? 0.0f : z[i];
             } else if (P.act == MOE_ACT_GELU) {
@@ -567,28 +698,28 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
               for (int i = 0; i < 32; ++i) z[i] = z[i] * sigmoid_f(z[i]);
             }
-          }
-          if constexpr (MODE == kFwd) {
+            uint8_t* buf = open_block();
             if (P.residual != nullptr) {
               // through the staging block to this lane's column; added in fp32
 #pragma unroll
-              for (int i = 0; i < kTok / 8; ++i) *piece(i * 8 + frow) = res[i];
+              for (int i = 0; i < kTok / 8; ++i) *piece(buf, i * 8 + frow) = res[i];
               __syncwarp();
 #pragma unroll
-              for (int i = 0; i < kTok; ++i) z[i] += bf16lo(*cell(i));
+              for (int i = 0; i < kTok; ++i) z[i] += bf16lo(*cell(buf, i));
             }
-          }
 #pragma unroll
-          for (int i = 0; i < kTok; ++i) *cell(i) = to_bf16(z[i]);
-          flush(P.out + (row_j + tok0) * P.M + ch0, (size_t)P.M, nr - tok0, nc, kTok / 8);
+            for (int i = 0; i < kTok; ++i) *cell(buf, i) = to_bf16(z[i]);
+            close_tokens(buf, &P.mo, P.out, row_j + tok0, ch0, P.M, kTok, nr - tok0, nc);
+          }
+        }
+        if (!empty_sum) {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(even_addr(&tempty[acc]));
         }
       }
-      if (!empty_sum) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(even_addr(&tempty[acc]));
-      }
     }
+    if (lane == 0) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -617,27 +748,34 @@ EncodeFn encode_fn() {
   return fn;
 }
 
-// bf16 tensor [d2][d1][d0] (d2 = 1: a matrix), boxes of 64 x box1, 128-byte
-// swizzle, zeros outside.
+// bf16 tensor [d2][d1][d0] (d2 = 0: a matrix), boxes of box0 x box1 (64 wide:
+// 128-byte swizzle, 32 wide: 64-byte), zeros outside.
 cudaError_t make_map(CUtensorMap* map, const void* ptr, int64_t d0, int64_t d1, int64_t d2,
-                     int box1) {
+                     int box0, int box1) {
   const EncodeFn fn = encode_fn();
   if (fn == nullptr) return cudaErrorNotSupported;
   const cuuint64_t dims[3] = {(cuuint64_t)d0, (cuuint64_t)d1, (cuuint64_t)d2};
   const cuuint64_t strides[2] = {(cuuint64_t)d0 * 2, (cuuint64_t)d0 * (cuuint64_t)d1 * 2};
-  const cuuint32_t box[3] = {64, (cuuint32_t)box1, 1};
+  const cuuint32_t box[3] = {(cuuint32_t)box0, (cuuint32_t)box1, 1};
   const cuuint32_t es[3] = {1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, d2 > 0 ? 3 : 2,
                         const_cast<void*>(ptr), dims, strides, box, es,
-                        CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        box0 == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+constexpr size_t kSmemLimit = 227 * 1024;
+constexpr size_t kSmemStatic = 1024;  // bounds the kernel's static shared memory
+
 template <int MODE, bool GATED>
-cudaError_t launch_gemm(const LaunchEnv& env, const GemmParams& P, int64_t max_tiles) {
-  const size_t smem = 1024 + (size_t)kStages * kStageBytes + kEpiBytes +
-                      sizeof(int32_t) * ((size_t)P.E * (MODE == kWeights ? 2 : 3) + 1);
+cudaError_t launch_gemm(const LaunchEnv& env, GemmParams& P, int64_t max_tiles) {
+  const size_t table = sizeof(int32_t) * ((size_t)P.E * (MODE == kWeights ? 2 : 3) + 1);
+  const size_t smem = kSmemLimit - kSmemStatic;
+  P.ring = (int)((smem - 1024 - kEpiBytes - table) / 1024 * 1024);
+  static_assert(kSmemLimit - kSmemStatic - 1024 - kEpiBytes - 12 * 1024 - 1024 >= 3 * kMaxSlice,
+                "three of the largest slices");
   int per_sm = 1;
   const auto kernel = expert_gemm_kernel<MODE, GATED>;
   cudaError_t err = blocks_per_sm((const void*)kernel, kGemmThreads, smem, &per_sm);
@@ -653,6 +791,32 @@ int64_t max_token_tiles(int64_t assignments, int E, int64_t bn) {
   return assignments / bn + (assignments < E ? assignments : E);
 }
 
+void segments_of(GemmParams& P, const ExpertMatmul& a) {
+  P.counts = a.counts;
+  P.off = a.expert_off;
+  P.hdr = a.hdr;
+  P.N = a.N;
+  P.max_rows = a.assignments;
+  P.E = a.E;
+  P.capacity = a.capacity;
+}
+
+// The token operand's maps, and the tiles' shape.
+cudaError_t token_operand(GemmParams& P, const ExpertMatmul& a, const void* rows, int cols) {
+  for (int i = 0; i < 3; ++i) {
+    const cudaError_t err = make_map(&P.mb[i], rows, cols, a.N, 0, 64, 32 << i);
+    if (err != cudaSuccess) return err;
+  }
+  P.kdim = cols;
+  P.band = 8;
+  P.max_n = 512;
+  return cudaSuccess;
+}
+
+int wide_features(const ExpertMatmul& a) {
+  return a.act == MOE_ACT_SWIGLU ? 2 * a.out_features : a.out_features;
+}
+
 }  // namespace
 
 bool expert_tiles_fit(int64_t assignments, int E, int in, int wide) {
@@ -663,27 +827,20 @@ bool expert_tiles_fit(int64_t assignments, int E, int in, int wide) {
 
 cudaError_t launch_expert_matmul(const LaunchEnv& env, const ExpertMatmul& a) {
   const bool gated = a.act == MOE_ACT_SWIGLU;
-  const int wide = gated ? 2 * a.out_features : a.out_features;
+  const int wide = wide_features(a);
   GemmParams P = {};
-  cudaError_t err = make_map(&P.ma, a.w, a.in_features, wide, a.E, gated ? kBM / 2 : kBM);
+  segments_of(P, a);
+  cudaError_t err = make_map(&P.ma, a.w, a.in_features, wide, a.E, 64, gated ? kBM / 2 : kBM);
+  if (err == cudaSuccess) err = token_operand(P, a, a.x, a.in_features);
+  if (err == cudaSuccess) err = make_map(&P.mo, a.out, a.out_features, a.N, 0, 32, gated ? 16 : 32);
+  if (err == cudaSuccess && a.pre != nullptr) err = make_map(&P.mp, a.pre, wide, a.N, 0, 32, 32);
   if (err != cudaSuccess) return err;
-  err = make_map(&P.mb, a.x, a.in_features, a.N, 0, kBox);
-  if (err != cudaSuccess) return err;
-  P.counts = a.counts;
-  P.off = a.expert_off;
   P.bias = a.bias;
   P.residual = static_cast<const uint16_t*>(a.residual);
   P.out = static_cast<uint16_t*>(a.out);
   P.pre = static_cast<uint16_t*>(a.pre);
-  P.hdr = a.hdr;
-  P.N = a.N;
-  P.max_rows = a.assignments;
-  P.E = a.E;
-  P.capacity = a.capacity;
   P.M = a.out_features;
-  P.kdim = a.in_features;
   P.act = a.act;
-  P.band = 16;
   const int64_t tt = max_token_tiles(a.assignments, a.E, kBN);
   if (gated) return launch_gemm<kFwd, true>(env, P, tt * ((P.M + kBM - 1) / kBM));
   return launch_gemm<kFwd, false>(env, P, tt * ((P.M + 2 * kBM - 1) / (2 * kBM)));
@@ -691,43 +848,29 @@ cudaError_t launch_expert_matmul(const LaunchEnv& env, const ExpertMatmul& a) {
 
 cudaError_t launch_expert_grad_rows(const LaunchEnv& env, const ExpertMatmul& a, const void* dz,
                                     void* grad_x) {
-  const int wide = a.act == MOE_ACT_SWIGLU ? 2 * a.out_features : a.out_features;
+  const int wide = wide_features(a);
   GemmParams P = {};
-  cudaError_t err = make_map(&P.ma, a.w, a.in_features, wide, a.E, kBK);
+  segments_of(P, a);
+  cudaError_t err = make_map(&P.ma, a.w, a.in_features, wide, a.E, 64, kBK);
+  if (err == cudaSuccess) err = token_operand(P, a, dz, wide);
+  if (err == cudaSuccess) err = make_map(&P.mo, grad_x, a.in_features, a.N, 0, 32, 32);
   if (err != cudaSuccess) return err;
-  err = make_map(&P.mb, dz, wide, a.N, 0, kBox);
-  if (err != cudaSuccess) return err;
-  P.counts = a.counts;
-  P.off = a.expert_off;
   P.out = static_cast<uint16_t*>(grad_x);
-  P.hdr = a.hdr;
-  P.N = a.N;
-  P.max_rows = a.assignments;
-  P.E = a.E;
-  P.capacity = a.capacity;
   P.M = a.in_features;
-  P.kdim = wide;
-  P.band = 16;
   const int64_t ct = (P.M + 2 * kBM - 1) / (2 * kBM);
   return launch_gemm<kRows, false>(env, P, max_token_tiles(a.assignments, a.E, kBN) * ct);
 }
 
 cudaError_t launch_expert_grad_weights(const LaunchEnv& env, const ExpertMatmul& a, const void* dz,
                                        void* grad_w) {
-  const int wide = a.act == MOE_ACT_SWIGLU ? 2 * a.out_features : a.out_features;
+  const int wide = wide_features(a);
   GemmParams P = {};
-  cudaError_t err = make_map(&P.ma, dz, wide, a.N, 0, kBK);
+  segments_of(P, a);
+  cudaError_t err = make_map(&P.ma, dz, wide, a.N, 0, 64, kBK);
+  if (err == cudaSuccess) err = make_map(&P.mb[0], a.x, a.in_features, a.N, 0, 64, kBK);
+  if (err == cudaSuccess) err = make_map(&P.mo, grad_w, a.in_features, wide, a.E, 32, 32);
   if (err != cudaSuccess) return err;
-  err = make_map(&P.mb, a.x, a.in_features, a.N, 0, kBK);
-  if (err != cudaSuccess) return err;
-  P.counts = a.counts;
-  P.off = a.expert_off;
   P.out = static_cast<uint16_t*>(grad_w);
-  P.hdr = a.hdr;
-  P.N = a.N;
-  P.max_rows = a.assignments;
-  P.E = a.E;
-  P.capacity = a.capacity;
   P.M = wide;
   P.cols = a.in_features;
   const int64_t tiles = (int64_t)a.E * ((wide + 2 * kBM - 1) / (2 * kBM)) *
