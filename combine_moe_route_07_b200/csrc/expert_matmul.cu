@@ -138,17 +138,38 @@ struct Tile {
 // rows alone a 256-column tile ran at 1230 TFLOP/s, with one of 128 at 1340.
 __device__ __forceinline__ int box_rows(int half) { return (half + 31) & ~31; }
 
+// The part of a wait that is not over at once; false: it gave up, or another
+// role of this CTA did.
+__device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, int* abort_flag,
+                                       WsHeader* hdr) {
+  volatile int* stop = abort_flag;
+  uint64_t t0 = 0;
+  for (unsigned it = 1; it < (1u << 24); ++it) {
+    if (mbar_try_wait(bar, parity)) return true;
+    if ((it & 63u) == 0u) {
+      const uint64_t now = global_ns();
+      if (t0 == 0) t0 = now;
+      if (*stop != 0 || now - t0 > kWaitNs) break;
+    }
+  }
+  if (*stop == 0) report(hdr, MOE_ERR_DEVICE_TIMEOUT, blockIdx.x);
+  *stop = 1;
+  return false;
+}
+
 template <int MODE, bool GATED>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     expert_gemm_kernel(const __grid_constant__ GemmParams P) {
   constexpr int kTileM = GATED ? kBM : 2 * kBM;  // output channels of a pair's tile
   extern __shared__ uint8_t smem_raw[];
-  // tempty and fixed are waited on by the even CTA only; full too, but for an odd
-  // CTA's slices with stale rows.  A slot's barriers see at most one phase at a
+  // full, tempty and fixed are waited on by the even CTA only.  A slot's barriers see at most one phase at a
   // time: the slot is used again only once the instructions that read it are done.
   __shared__ uint64_t full[kSlots], empty[kSlots], tfull[2], tempty[2], drain;
-  __shared__ uint64_t fixed[kSlots];  // weights gradient: the odd CTA's stale rows are zero
+  // weights gradient, slices with stale rows: this CTA's half has landed; both
+  // CTAs' stale rows are zero
+  __shared__ uint64_t landed[kSlots], fixed[kSlots];
   __shared__ uint64_t swap[4];      // gated: between the two warps of a channel block
+  __shared__ int taken[2][kSlots];  // producers: bytes of the slices in flight
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ unsigned long long rows_sum;
@@ -167,7 +188,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     for (int s = 0; s < kSlots; ++s) {
       mbar_init(&full[s], 1);
       mbar_init(&empty[s], 1);
-      mbar_init(&fixed[s], 1);
+      mbar_init(&landed[s], 1);
+      mbar_init(&fixed[s], 2);
     }
     for (int s = 0; s < 2; ++s) {
       mbar_init(&tfull[s], 1);
@@ -219,20 +241,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   volatile int* stop = &abort_flag;
   // Wait for a phase; false: it gave up, or another role did.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
-    uint64_t t0 = 0;  // the clock is read only by waits that take long: it is slow
-    for (unsigned it = 1; it < (1u << 24); ++it) {
-      if (mbar_try_wait_cluster(bar, parity)) return true;
-      if ((it & 63u) == 0u) {
-        const uint64_t now = global_ns();
-        if (t0 == 0) t0 = now;
-        if (*stop != 0 || now - t0 > kWaitNs) break;
-      }
-    }
-    if (*stop == 0) report(P.hdr, MOE_ERR_DEVICE_TIMEOUT, blockIdx.x);
-    *stop = 1;
-    return false;
+    if (mbar_try_wait(bar, parity)) return true;
+    return wait_long(bar, parity, &abort_flag, P.hdr);
   };
-
   // The same for a whole warp: one answer for all its lanes.
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     return __all_sync(kFull, wait(bar, parity));
@@ -292,198 +303,186 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   };
   // Rows of the last slice that belong to the expert, when fewer than its
   // 16-deep steps take in (weights gradient).
-  auto stale_tail = [&](int depth, int kb) -> bool {
-    return MODE == kWeights && (kb + 1) * kBK > depth && (depth & 15) != 0;
+  auto stale_tail = [&](int depth, int k0) -> bool {
+    return MODE == kWeights && k0 + kBK > depth && (depth & 15) != 0;
   };
   // Rows behind the expert's last one are another expert's, or never written.
   // Steps wholly behind it are skipped; in the last step they become zero in
   // both operands (zero times NaN is not zero).  One warp, on this CTA's half.
-  auto zero_stale = [&](uint8_t* stage, int depth, int kb, int blocks) {
-    const int valid = depth - kb * kBK, stale = 16 - (valid & 15);
+  auto zero_stale = [&](uint8_t* slice, int depth, int k0, int blocks) {
+    const int valid = depth - k0, stale = 16 - (valid & 15);
     for (int i = lane; i < blocks * stale * 8; i += 32) {
       const int q = i & 7, row = valid + (i >> 3) % stale, blk = (i >> 3) / stale;
-      *reinterpret_cast<uint4*>(stage + blk * 8192 + row * 128 + q * 16) = make_uint4(0, 0, 0, 0);
+      *reinterpret_cast<uint4*>(slice + blk * 8192 + row * 128 + q * 16) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
     __syncwarp();
   };
 
-  if (wid == 0) {
-    // ---- producer -------------------------------------------------------------
+  if (wid == 0 || wid == 2) {
+    // ---- producers: warp 0 the M operand, warp 2 the N operand --------------------
+    // One thread each: a single thread issuing both took about 900 cycles a slice,
+    // longer than HBM needs to bring a narrow one.
     if (lane == 0) {
       uint32_t it = 0, old = 0;  // slices issued, and those known to be used up
-      int head = 0, room = P.ring >> 10;
-      uint64_t taken = 0;  // byte s: KiB that slot s's slice took, the gap before it too
-      const uint32_t even_full = even_addr(&full[0]);
+      int head = 0, room = P.ring;
+      int* const mine = taken[wid >> 1];
+      const uint32_t even_full = even_addr(&full[0]), own_landed = smem_addr(&landed[0]);
       bool ok = true;
       for (int t = pair; t < total && ok; t += pairs) {
         const Tile r = tile_of(t);
         const int depth = MODE == kWeights ? seg_rows[r.e] : P.kdim;
-        const int nkb = (depth + kBK - 1) / kBK;
         const int half = r.n / 2;  // columns of an accumulator from each CTA's operand
         const int bytes = slice_bytes(r);
         const int row = seg_off[r.e] + (MODE == kWeights ? 0 : r.row0 + (int)rank * half);
         const int col = r.row0 + (int)rank * half;  // weights gradient
         const int ch = r.c * kTileM + (int)rank * (GATED ? kBM / 2 : kBM);
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          const int s = it % kSlots;
-          const int gap = head + bytes > P.ring ? P.ring - head : 0;
-          const int at = place(head, bytes);
-          const int need = (bytes + gap) >> 10;
+        const int fetched = box_rows(half);
+        for (int k0 = 0; k0 < depth; k0 += kBK, ++it) {
+          const uint32_t s = it % kSlots;
+          int need = bytes;
+          if (head + bytes > P.ring) {  // (as place())
+            need += P.ring - head;
+            head = 0;
+          }
           // the oldest slices make room: for the bytes, and for the slot
           while (room < need || it - old == kSlots) {
-            const int o = old % kSlots;
+            const uint32_t o = old % kSlots;
             if (!wait(&empty[o], (old / kSlots) & 1u)) {
               ok = false;
               break;
             }
-            room += (int)((taken >> (8 * o)) & 255u);
+            room += mine[o];
             ++old;
           }
           if (!ok) break;
           room -= need;
-          taken = (taken & ~(255ull << (8 * s))) | ((uint64_t)need << (8 * s));
-          uint8_t* a = smem + at;
-          uint8_t* b = a + kABytes;
-          // both CTAs' copies complete on the even CTA's barrier, except that an odd CTA's
-          // slice with stale rows passes through that CTA's hands first
-          uint32_t bar = even_full + s * 8;
-          const bool apart = stale_tail(depth, kb);
-          if (rank == 0) {
-            mbar_arrive_expect_tx(&full[s], (uint32_t)(apart ? bytes : 2 * bytes));
-          } else if (apart) {
-            mbar_arrive_expect_tx(&full[s], (uint32_t)bytes);
-            bar = smem_addr(&full[s]);
-          }
-          if constexpr (MODE == kWeights) {
-            tma_load_2d(a, &P.ma, ch, row + kb * kBK, bar);
-            tma_load_2d(a + 8192, &P.ma, ch + 64, row + kb * kBK, bar);
-            tma_load_2d(b, &P.mb[0], col, row + kb * kBK, bar);
-            if (half > 64) tma_load_2d(b + 8192, &P.mb[0], col + 64, row + kb * kBK, bar);
-          } else {
-            if constexpr (MODE == kFwd) {
-              tma_load_3d(a, &P.ma, kb * kBK, ch, r.e, bar);
-              if constexpr (GATED)
-                tma_load_3d(a + kABytes / 2, &P.ma, kb * kBK, P.M + ch, r.e, bar);
+          mine[s] = need;
+          uint8_t* a = smem + head;
+          head += bytes;
+          // both CTAs' copies complete on the even CTA's barrier; of slices with stale
+          // rows each CTA's on its own, whose fixer passes them on
+          const bool apart = stale_tail(depth, k0);
+          const uint32_t bar = (apart ? own_landed : even_full) + s * 8;
+          if (wid == 0) {
+            if (apart)
+              mbar_arrive_expect_tx(&landed[s], (uint32_t)bytes);
+            else if (rank == 0)
+              mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * bytes));
+            if constexpr (MODE == kWeights) {
+              tma_load_2d(a, &P.ma, ch, row + k0, bar);
+              tma_load_2d(a + 8192, &P.ma, ch + 64, row + k0, bar);
+            } else if constexpr (MODE == kFwd) {
+              tma_load_3d(a, &P.ma, k0, ch, r.e, bar);
+              if constexpr (GATED) tma_load_3d(a + kABytes / 2, &P.ma, k0, P.M + ch, r.e, bar);
             } else {
-              tma_load_3d(a, &P.ma, ch, kb * kBK, r.e, bar);
-              tma_load_3d(a + 8192, &P.ma, ch + 64, kb * kBK, r.e, bar);
+              tma_load_3d(a, &P.ma, ch, k0, r.e, bar);
+              tma_load_3d(a + 8192, &P.ma, ch + 64, k0, r.e, bar);
             }
-            const int fetched = box_rows(half);
-            for (int p = 0; p < r.parts; ++p) {
-              uint8_t* bp = b + p * fetched * (kBK * 2);
-              const int y = row + p * r.n;
-              if (fetched == 128) {
-                tma_load_2d(bp, &P.mb[2], kb * kBK, y, bar);
-              } else {
-                int done = 0;
-                if (fetched >= 64) {
-                  tma_load_2d(bp, &P.mb[1], kb * kBK, y, bar);
-                  done = 64;
+          } else {
+            uint8_t* b = a + kABytes;
+            if constexpr (MODE == kWeights) {
+              tma_load_2d(b, &P.mb[0], col, row + k0, bar);
+              if (half > 64) tma_load_2d(b + 8192, &P.mb[0], col + 64, row + k0, bar);
+            } else {
+              int y = row;
+              for (int p = 0; p < r.parts; ++p, y += r.n, b += fetched * (kBK * 2)) {
+                if (fetched == 128) {
+                  tma_load_2d(b, &P.mb[2], k0, y, bar);
+                } else if (fetched == 32) {
+                  tma_load_2d(b, &P.mb[0], k0, y, bar);
+                } else {
+                  tma_load_2d(b, &P.mb[1], k0, y, bar);
+                  if (fetched == 96) tma_load_2d(b + 8192, &P.mb[0], k0, y + 64, bar);
                 }
-                if (fetched > done) tma_load_2d(bp + done * (kBK * 2), &P.mb[0], kb * kBK, y + done, bar);
               }
             }
           }
         }
       }
-      if (!ok) {  // copies in flight land before the pair ends
-        if (rank == 0)
-          for (uint32_t j = old; j < it; ++j)
-            mbar_wait_bounded(&full[j % kSlots], (j / kSlots) & 1u, 1000000ull);
-        else
-          mbar_wait_bounded(&drain, 0u, 1000000ull);  // a pause
+      if (!ok) {  // copies in flight land before the pair ends: they take microseconds
+        const uint64_t t0 = global_ns();
+        for (int i = 0; i < 100000 && global_ns() - t0 < 2000000ull; ++i) __nanosleep(1000);
       }
     }
     __syncwarp();
   } else if (wid == 1 && rank == 0) {
-    // ---- matrix instructions ----------------------------------------------------
-    constexpr uint32_t a_mn = MODE == kFwd ? 0u : 1u, b_mn = MODE == kWeights ? 1u : 0u;
-    uint32_t it = 0, nacc = 0, fix_par = 0;  // bit s: parity of fixed[s]'s next phase
-    int head = 0;
-    bool ok = true;
-    for (int t = pair; t < total && ok; t += pairs) {
-      const Tile r = tile_of(t);
-      const int depth = MODE == kWeights ? seg_rows[r.e] : P.kdim;
-      const int nkb = (depth + kBK - 1) / kBK;
-      if (nkb == 0) continue;
-      for (int p = 0; p < r.parts && ok; ++p)
-        ok = warp_wait(&tempty[(nacc + p) & 1u], (((nacc + p) >> 1) & 1u) ^ 1u);
-      if (!ok) break;
-      tc_fence_after();
-      const uint32_t idesc = umma_idesc(2 * kBM, (uint32_t)r.n, a_mn, b_mn);
-      const int bytes = slice_bytes(r);
-      const uint32_t part_bytes = (uint32_t)((bytes - kABytes) / r.parts);
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        const int s = it % kSlots;
-        const int at = place(head, bytes);
-        if (!warp_wait(&full[s], (it / kSlots) & 1u)) {
-          ok = false;
-          break;
-        }
-        int ksteps = kBK / 16;
-        if constexpr (MODE == kWeights) ksteps = (min(kBK, depth - kb * kBK) + 15) >> 4;
-        if (stale_tail(depth, kb)) {
-          zero_stale(smem + at, depth, kb, bytes / 8192);
-          if (!warp_wait(&fixed[s], (fix_par >> s) & 1u)) {
-            ok = false;
-            break;
-          }
-          fix_par ^= 1u << s;
-        }
+    // ---- matrix instructions: one thread of the even CTA --------------------------
+    if (lane == 0) {
+      constexpr uint32_t a_mn = MODE == kFwd ? 0u : 1u, b_mn = MODE == kWeights ? 1u : 0u;
+      // a 16-deep step further: 32 bytes along K-major rows, 2048 over MN-major ones
+      constexpr uint64_t sa16 = a_mn ? 128 : 2, sb16 = b_mn ? 128 : 2;
+      const uint64_t da_ring = a_mn ? umma_desc(smem_addr(smem), 8192, 1024)
+                                    : umma_desc(smem_addr(smem), 16, 1024);
+      const uint64_t db_ring = b_mn ? umma_desc(smem_addr(smem) + kABytes, 8192, 1024)
+                                    : umma_desc(smem_addr(smem) + kABytes, 16, 1024);
+      uint32_t it = 0, nacc = 0;
+      uint32_t full_par = 0, fix_par = 0;  // bit s: parity of full[s]'s, fixed[s]'s next phase
+      int head = 0;
+      bool ok = true;
+      for (int t = pair; t < total && ok; t += pairs) {
+        const Tile r = tile_of(t);
+        const int depth = MODE == kWeights ? seg_rows[r.e] : P.kdim;
+        if (depth == 0) continue;
+        for (int p = 0; p < r.parts && ok; ++p)
+          ok = wait(&tempty[(nacc + p) & 1u], (((nacc + p) >> 1) & 1u) ^ 1u);
+        if (!ok) break;
         tc_fence_after();
-        if (lane == 0) {
-          const uint32_t sa = smem_addr(smem + at), sb = sa + kABytes;
-          const uint64_t da = a_mn ? umma_desc(sa, 8192, 1024) : umma_desc(sa, 16, 1024);
-          const uint64_t db = b_mn ? umma_desc(sb, 8192, 1024) : umma_desc(sb, 16, 1024);
-          // a 16-deep step further: 32 bytes along K-major rows, 2048 over MN-major ones
-          constexpr uint64_t sa16 = a_mn ? 128 : 2, sb16 = b_mn ? 128 : 2;
-          const uint32_t d0 = tmem + (nacc & 1u) * 256u;
+        const uint32_t idesc = umma_idesc(2 * kBM, (uint32_t)r.n, a_mn, b_mn);
+        const int bytes = slice_bytes(r);
+        const uint64_t part = (uint64_t)(r.parts == 2 ? (bytes - kABytes) / 32 : 0);
+        const uint32_t d0 = tmem + (nacc & 1u) * 256u, d1 = tmem + (~nacc & 1u) * 256u;
+        for (int k0 = 0; k0 < depth; k0 += kBK, ++it) {
+          const uint32_t s = it % kSlots;
+          const int at = place(head, bytes);
+          if (stale_tail(depth, k0)) {
+            ok = wait(&fixed[s], (fix_par >> s) & 1u);
+            // the zeros are generic writes of both CTAs: acquired at cluster scope
+            mbar_try_wait_cluster(&fixed[s], (fix_par >> s) & 1u);
+            fix_par ^= 1u << s;
+          } else {
+            ok = wait(&full[s], (full_par >> s) & 1u);
+            full_par ^= 1u << s;
+          }
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t da = da_ring + (uint32_t)(at >> 4), db = db_ring + (uint32_t)(at >> 4);
+          const int ksteps = MODE == kWeights ? (min(kBK, depth - k0) + 15) >> 4 : kBK / 16;
 #pragma unroll
           for (int q = 0; q < kBK / 16; ++q)
             if (MODE != kWeights || q < ksteps)
-              umma_f16(d0, da + q * sa16, db + q * sb16, idesc, kb > 0 || q > 0);
-          if (r.parts == 2) {
-            const uint64_t db1 = db + (part_bytes >> 4);
-            const uint32_t d1 = tmem + (~nacc & 1u) * 256u;
+              umma_f16(d0, da + q * sa16, db + q * sb16, idesc, k0 > 0 || q > 0);
+          if (MODE != kWeights && r.parts == 2) {
 #pragma unroll
             for (int q = 0; q < kBK / 16; ++q)
-              umma_f16(d1, da + q * sa16, db1 + q * sb16, idesc, kb > 0 || q > 0);
+              umma_f16(d1, da + q * sa16, db + part + q * sb16, idesc, k0 > 0 || q > 0);
           }
           umma_commit(&empty[s]);
         }
-        __syncwarp();
+        if (!ok) break;
+        for (int p = 0; p < r.parts; ++p, ++nacc) umma_commit(&tfull[nacc & 1u]);
       }
-      if (!ok) break;
-      for (int p = 0; p < r.parts; ++p, ++nacc)
-        if (lane == 0) umma_commit(&tfull[nacc & 1u]);
-      __syncwarp();
-    }
-    if (*stop != 0) {
-      if (lane == 0) {
+      if (!ok) {  // what was issued ends before the pair does
         umma_commit(&drain);
         mbar_wait_bounded(&drain, 0u, kWaitNs);
       }
-      __syncwarp();
     }
-  } else if (wid == 1 && MODE == kWeights) {
-    // ---- odd CTA: its stale rows ------------------------------------------------
-    uint32_t it = 0, par = 0;  // bit s: parity of full[s]'s next phase here
+    __syncwarp();
+  } else if (wid == 3 && MODE == kWeights) {
+    // ---- fixer: zeros for the stale rows of this CTA's half -------------------------
+    uint32_t it = 0, par = 0;  // bit s: parity of landed[s]'s next phase
     int head = 0;
     for (int t = pair; t < total; t += pairs) {
       const Tile r = tile_of(t);
       const int depth = seg_rows[r.e];
-      const int nkb = (depth + kBK - 1) / kBK;
-      if (nkb == 0) continue;
       const int bytes = slice_bytes(r);
-      for (int kb = 0; kb < nkb - 1; ++kb) place(head, bytes);
-      const int at = place(head, bytes);
-      it += nkb;
-      if (stale_tail(depth, nkb - 1)) {
-        const int s = (int)((it - 1) % kSlots);
-        if (!warp_wait(&full[s], (par >> s) & 1u)) break;
+      for (int k0 = 0; k0 < depth; k0 += kBK, ++it) {
+        const int at = place(head, bytes);
+        if (!stale_tail(depth, k0)) continue;
+        const uint32_t s = it % kSlots;
+        if (!warp_wait(&landed[s], (par >> s) & 1u)) break;
         par ^= 1u << s;
-        zero_stale(smem + at, depth, nkb - 1, bytes / 8192);
+        zero_stale(smem + at, depth, k0, bytes / 8192);
         if (lane == 0) mbar_arrive_cluster(even_addr(&fixed[s]));
       }
     }
