@@ -71,6 +71,7 @@ struct GemmParams {
   int band;    // token tiles an expert walks together
   int max_n;   // columns of a tile, at most (256 or 512)
   int ring;    // bytes of the operand ring
+  int sorted;  // experts in descending order of their rows (see my_tile)
   int act;
 };
 
@@ -130,7 +131,7 @@ __device__ __forceinline__ uint16_t to_bf16(float v) {
 // A tile: its expert, channel tile, first row (weights gradient: column) and
 // rows; one or two accumulators ("parts") of `n` columns each.
 struct Tile {
-  int e, c, row0, rows, parts, n;
+  int e, seg, c, row0, rows, parts, n;  // seg: the expert's place in the segment table
 };
 
 // Token rows that copies bring for `half` (a multiple of 16, up to 128) wanted:
@@ -179,7 +180,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   uint8_t* epi = smem + P.ring;
   int32_t* seg_off = reinterpret_cast<int32_t*>(epi + kEpiBytes);
   int32_t* seg_rows = seg_off + P.E;
-  int32_t* first = seg_rows + P.E;  // forward / rows: exclusive prefix of token tiles [E+1]
+  // forward / rows: exclusive prefix of token tiles [E+1], and the experts in the
+  // table's order [E]
+  int32_t* first = seg_rows + P.E;
+  int32_t* expert = first + P.E + 1;
 
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const uint32_t rank = cluster_rank();
@@ -208,14 +212,49 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   pdl_wait();
   pdl_trigger();
   unsigned long long my_rows = 0ull;
-  for (int e = tid; e < P.E; e += kGemmThreads) {
-    const Segment s = segment(P, e, blockIdx.x == 0);
-    seg_off[e] = s.off;
-    seg_rows[e] = s.rows;
-    my_rows += (unsigned long long)s.rows;
-    if (MODE != kWeights) first[e] = (s.rows + P.max_n - 1) / P.max_n;
+  constexpr int kMine = (1024 + kGemmThreads - 1) / kGemmThreads;
+  Segment seg[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int e = tid + i * kGemmThreads;
+    if (e < P.E) {
+      seg[i] = segment(P, e, blockIdx.x == 0);
+      my_rows += (unsigned long long)seg[i].rows;
+      if (MODE != kWeights && P.sorted) first[e] = seg[i].rows;
+    }
   }
   if (my_rows != 0ull) atomicAdd(&rows_sum, my_rows);
+  int at[kMine];
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) at[i] = tid + i * kGemmThreads;
+  if (MODE != kWeights && P.sorted) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kMine; ++i) {
+      const int e = tid + i * kGemmThreads;
+      if (e < P.E) {
+        int before = 0;
+        for (int j = 0; j < P.E; ++j) {
+          const int rj = first[j];
+          before += (rj > seg[i].rows || (rj == seg[i].rows && j < e)) ? 1 : 0;
+        }
+        at[i] = before;
+      }
+    }
+    __syncthreads();
+  }
+#pragma unroll
+  for (int i = 0; i < kMine; ++i) {
+    const int e = tid + i * kGemmThreads;
+    if (e < P.E) {
+      seg_off[at[i]] = seg[i].off;
+      seg_rows[at[i]] = seg[i].rows;
+      if (MODE != kWeights) {
+        first[at[i]] = (seg[i].rows + P.max_n - 1) / P.max_n;
+        expert[at[i]] = e;
+      }
+    }
+  }
   tc_fence_before();
   __syncthreads();
   cluster_sync_all();  // the other CTA's barriers are ready too
@@ -238,7 +277,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     total = 0;
   }
 
-  volatile int* stop = &abort_flag;
   // Wait for a phase; false: it gave up, or another role did.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     if (mbar_try_wait(bar, parity)) return true;
@@ -254,7 +292,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     Tile r;
     if constexpr (MODE == kWeights) {
       const int nt = (P.cols + kBN - 1) / kBN;
-      r.e = t / (ctiles * nt);
+      r.e = r.seg = t / (ctiles * nt);
       const int u = t - r.e * ctiles * nt;
       r.c = u / nt;
       r.row0 = (u - r.c * nt) * kBN;  // first column
@@ -279,7 +317,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const int n = b * P.band + v % nb;
       // the rows split evenly over the expert's tiles, in multiples of 32
       const int per = ((seg_rows[lo] + nt - 1) / nt + 31) & ~31;
-      r.e = lo;
+      r.e = expert[lo];
+      r.seg = lo;
       r.c = v / nb;
       r.row0 = n * per;
       r.rows = min(per, seg_rows[lo] - r.row0);
@@ -288,6 +327,23 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
     return r;
   };
+  // The j-th tile of this pair, -1 if it has none in that round.  Tiles are dealt
+  // out in rounds.  Sorted experts: every second round in reverse, so that each
+  // pair gets about the same work, and half of the pairs walk their rounds
+  // backwards, so that large tiles (bound by the tensor cores) and small ones
+  // (bound by HBM) run side by side.
+  const int rounds = (total + pairs - 1) / pairs;
+  auto my_tile = [&](int j) -> int {
+    int t;
+    if (MODE != kWeights && P.sorted) {
+      const int round = pair < (pairs >> 1) ? j : rounds - 1 - j;
+      t = round * pairs + ((round & 1) ? pairs - 1 - pair : pair);
+    } else {
+      t = j * pairs + pair;
+    }
+    return t < total ? t : -1;
+  };
+
   // The ring: a slice of a tile takes the bytes it needs (the M operand's 16 KiB and
   // the rows of the N operand), behind the one before it or, where it does not fit
   // there, at the ring's start.  Every role places the slices alike.
@@ -321,20 +377,20 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 
   if (wid == 0 || wid == 2) {
     // ---- producers: warp 0 the M operand, warp 2 the N operand --------------------
-    // One thread each: a single thread issuing both took about 900 cycles a slice,
-    // longer than HBM needs to bring a narrow one.
-    if (lane == 0) {
+    if (elect_one()) {
       uint32_t it = 0, old = 0;  // slices issued, and those known to be used up
       int head = 0, room = P.ring;
       int* const mine = taken[wid >> 1];
       const uint32_t even_full = even_addr(&full[0]), own_landed = smem_addr(&landed[0]);
       bool ok = true;
-      for (int t = pair; t < total && ok; t += pairs) {
+      for (int j = 0; j < rounds && ok; ++j) {
+        const int t = my_tile(j);
+        if (t < 0) continue;
         const Tile r = tile_of(t);
-        const int depth = MODE == kWeights ? seg_rows[r.e] : P.kdim;
+        const int depth = MODE == kWeights ? seg_rows[r.seg] : P.kdim;
         const int half = r.n / 2;  // columns of an accumulator from each CTA's operand
         const int bytes = slice_bytes(r);
-        const int row = seg_off[r.e] + (MODE == kWeights ? 0 : r.row0 + (int)rank * half);
+        const int row = seg_off[r.seg] + (MODE == kWeights ? 0 : r.row0 + (int)rank * half);
         const int col = r.row0 + (int)rank * half;  // weights gradient
         const int ch = r.c * kTileM + (int)rank * (GATED ? kBM / 2 : kBM);
         const int fetched = box_rows(half);
@@ -408,7 +464,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     __syncwarp();
   } else if (wid == 1 && rank == 0) {
     // ---- matrix instructions: one thread of the even CTA --------------------------
-    if (lane == 0) {
+    if (elect_one()) {
       constexpr uint32_t a_mn = MODE == kFwd ? 0u : 1u, b_mn = MODE == kWeights ? 1u : 0u;
       // a 16-deep step further: 32 bytes along K-major rows, 2048 over MN-major ones
       constexpr uint64_t sa16 = a_mn ? 128 : 2, sb16 = b_mn ? 128 : 2;
@@ -420,9 +476,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       uint32_t full_par = 0, fix_par = 0;  // bit s: parity of full[s]'s, fixed[s]'s next phase
       int head = 0;
       bool ok = true;
-      for (int t = pair; t < total && ok; t += pairs) {
+      for (int j = 0; j < rounds && ok; ++j) {
+        const int t = my_tile(j);
+        if (t < 0) continue;
         const Tile r = tile_of(t);
-        const int depth = MODE == kWeights ? seg_rows[r.e] : P.kdim;
+        const int depth = MODE == kWeights ? seg_rows[r.seg] : P.kdim;
         if (depth == 0) continue;
         for (int p = 0; p < r.parts && ok; ++p)
           ok = wait(&tempty[(nacc + p) & 1u], (((nacc + p) >> 1) & 1u) ^ 1u);
@@ -472,9 +530,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     // ---- fixer: zeros for the stale rows of this CTA's half -------------------------
     uint32_t it = 0, par = 0;  // bit s: parity of landed[s]'s next phase
     int head = 0;
-    for (int t = pair; t < total; t += pairs) {
+    for (int j = 0; j < rounds; ++j) {
+      const int t = my_tile(j);
+      if (t < 0) continue;
       const Tile r = tile_of(t);
-      const int depth = seg_rows[r.e];
+      const int depth = seg_rows[r.seg];
       const int bytes = slice_bytes(r);
       for (int k0 = 0; k0 < depth; k0 += kBK, ++it) {
         const int at = place(head, bytes);
@@ -502,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     // A staging block.  Every use is one bulk group, empty or not: with at most one
     // group still reading, the use before last is done.
     auto open_block = [&]() -> uint8_t* {
-      if (lane == 0) bulk_wait_read<1>();
+      if (elect_one()) bulk_wait_read<1>();
       __syncwarp();
       return blocks + (uses++ & 1u) * 2048;
     };
@@ -522,7 +582,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       if (nrows >= box) {
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) {
+        if (elect_one()) {
           if (ncols > 0) tma_store_2d(map, buf, ch, (int)row);
           bulk_commit();
         }
@@ -535,14 +595,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           if (rr < nrows && fcol < ncols) st16(dst + (size_t)rr * stride + fcol, *piece(buf, rr));
         }
         __syncwarp();
-        if (lane == 0) bulk_commit();
+        if (elect_one()) bulk_commit();
       }
     };
     uint32_t nacc = 0, nswap = 0;
     bool ok = true;
-    for (int t = pair; t < total && ok; t += pairs) {
+    for (int i = 0; i < rounds && ok; ++i) {
+      const int t = my_tile(i);
+      if (t < 0) continue;
       const Tile r = tile_of(t);
-      const bool empty_sum = MODE == kWeights && seg_rows[r.e] == 0;
+      const bool empty_sum = MODE == kWeights && seg_rows[r.seg] == 0;
       // this warp's first channel (gated: of the half that it holds)
       const int ch0 = GATED ? r.c * kTileM + (int)rank * 64 + (q & 1) * 32
                             : r.c * kTileM + (int)rank * kBM + q * 32;
@@ -576,7 +638,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             }
             fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) {
+            if (elect_one()) {
               if (nc > 0) tma_store_3d(&P.mo, buf, row0 + j * 32, ch0, r.e);
               bulk_commit();
             }
@@ -596,7 +658,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           }
         } else if constexpr (MODE == kRows) {
           // this lane holds one channel of 32 tokens: staged token-major
-          const int64_t row = (int64_t)seg_off[r.e] + row0;
+          const int64_t row = (int64_t)seg_off[r.seg] + row0;
           auto stage = [&](const uint32_t(&v)[32], int j) {
             uint8_t* buf = open_block();
 #pragma unroll
@@ -617,7 +679,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           float b0 = 0.0f;
           if (P.bias != nullptr && ch < P.M)
             b0 = __ldg(P.bias + (size_t)r.e * P.M * (GATED ? 2 : 1) + (up_half ? P.M : 0) + ch);
-          const int64_t row = (int64_t)seg_off[r.e] + row0;
+          const int64_t row = (int64_t)seg_off[r.seg] + row0;
           for (int j = half; j < nchunks; j += 2) {
             const int64_t row_j = row + j * 32;
             const int nr = rows - j * 32;
@@ -665,7 +727,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
               for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = up_half ? z[i] : z[16 + i];
               __syncwarp();
-              if (lane == 0) {
+              if (elect_one()) {
                 bulk_commit();
                 mbar_arrive(bar);
               }
@@ -718,7 +780,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         }
       }
     }
-    if (lane == 0) bulk_wait_all();
+    if (elect_one()) bulk_wait_all();
   }
   tc_fence_before();
   __syncthreads();
@@ -770,10 +832,10 @@ constexpr size_t kSmemStatic = 1024;  // bounds the kernel's static shared memor
 
 template <int MODE, bool GATED>
 cudaError_t launch_gemm(const LaunchEnv& env, GemmParams& P, int64_t max_tiles) {
-  const size_t table = sizeof(int32_t) * ((size_t)P.E * (MODE == kWeights ? 2 : 3) + 1);
+  const size_t table = sizeof(int32_t) * ((size_t)P.E * (MODE == kWeights ? 2 : 4) + 1);
   const size_t smem = kSmemLimit - kSmemStatic;
   P.ring = (int)((smem - 1024 - kEpiBytes - table) / 1024 * 1024);
-  static_assert(kSmemLimit - kSmemStatic - 1024 - kEpiBytes - 12 * 1024 - 1024 >= 3 * kMaxSlice,
+  static_assert(kSmemLimit - kSmemStatic - 1024 - kEpiBytes - 16 * 1024 - 1024 >= 3 * kMaxSlice,
                 "three of the largest slices");
   int per_sm = 1;
   const auto kernel = expert_gemm_kernel<MODE, GATED>;
@@ -809,6 +871,8 @@ cudaError_t token_operand(GemmParams& P, const ExpertMatmul& a, const void* rows
   P.kdim = cols;
   P.band = 8;
   P.max_n = 512;
+  // ranking costs E^2 / 384 steps a CTA: where tiles are large enough to differ
+  P.sorted = a.E > 1 && a.assignments >= (int64_t)32 * a.E;
   return cudaSuccess;
 }
 

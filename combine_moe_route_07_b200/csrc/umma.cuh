@@ -11,6 +11,17 @@ namespace moe {
 // Every wrapper here is for a pair of CTAs (cta_group::2): the even CTA of a
 // cluster of two issues matrix instructions over both CTAs' operands.
 
+// True in one lane of a converged warp.  Tensor-map copies and matrix
+// instructions take their operands from uniform registers; behind a test of the
+// lane number the compiler has to reckon with several active lanes and wraps
+// each of them in a loop over the lanes, behind elect.sync it does not.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile(
+      "{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
+  return p != 0;
+}
+
 // ---- tensor memory ----------------------------------------------------------
 // One warp of each CTA allocates and frees.  The base address is written to *slot.
 __device__ __forceinline__ void tmem_alloc(uint32_t* slot, uint32_t cols) {
