@@ -122,12 +122,6 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-__device__ __forceinline__ uint16_t to_bf16(float v) {
-  uint16_t r;
-  asm("cvt.rn.bf16.f32 %0, %1;" : "=h"(r) : "f"(v));
-  return r;
-}
-
 // A tile: its expert, channel tile, first row (weights gradient: column) and
 // rows; one or two accumulators ("parts") of `n` columns each.
 struct Tile {
@@ -570,10 +564,24 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     auto piece = [&](uint8_t* buf, int row) {
       return reinterpret_cast<uint4*>(buf + row * 64 + (((lane & 3) ^ ((row >> 1) & 3)) << 4));
     };
-    // this lane's column of a staged row
-    auto cell = [&](uint8_t* buf, int row) {
-      return reinterpret_cast<uint16_t*>(buf) + row * 32 +
-             (((lane >> 3) ^ ((row >> 1) & 3)) << 3) + (lane & 7);
+    // Products by channel: a block of 32 channels x 32 tokens sits in fragments (see
+    // tmem_ld16): value (h, j, i) of a thread, at 16h + 4j + i, is channel 16h + 8(i/2)
+    // + lane/4 of token 8j + 2(lane%4) + i%2.  Four transposing block stores a block
+    // bring it token-major into shared memory (one 2-byte store a value cost half as
+    // much again as everything else here).
+    const uint32_t t_addr =
+        (uint32_t)((lane & 7) * 64 + (((lane >> 3) ^ ((lane & 7) >> 1)) << 4));
+    auto load_block = [&](uint32_t addr, uint32_t(&v)[32]) {
+      tmem_ld16(addr, v);
+      tmem_ld16(addr + (16u << 16), v + 16);
+    };
+    // tokens 8j..8j+7 of z (row stride of a fragment group: 4 nj values) -> staged rows
+    // 8r..8r+7
+    auto stage8 = [&](uint8_t* buf, int r, const float* z, int j, int nj) {
+      const float* a = z + 4 * j;
+      const float* b = z + 4 * nj + 4 * j;
+      stmatrix_t(smem_addr(buf) + t_addr + r * 512, pack2(a[0], a[1]), pack2(a[2], a[3]),
+                 pack2(b[0], b[1]), pack2(b[2], b[3]));
     };
     // Token-major block of `box` rows at (row, ch) of a matrix `stride` wide, of which
     // `nrows` rows and `ncols` columns (a multiple of 8) are this expert's.
@@ -648,7 +656,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             if (!empty_sum) {
               tmem_ld32(d + j * 32, v0);
               if (j + 2 < nchunks) tmem_ld32(d + j * 32 + 64, v1);
-              tmem_ld_wait();
+              tmem_ld_wait(v0);
+              tmem_ld_wait(v1);
             } else {
 #pragma unroll
               for (int i = 0; i < 32; ++i) v0[i] = v1[i] = 0u;
@@ -656,30 +665,21 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             stage(v0, j);
             if (j + 2 < nchunks) stage(v1, j + 2);
           }
-        } else if constexpr (MODE == kRows) {
-          // this lane holds one channel of 32 tokens: staged token-major
-          const int64_t row = (int64_t)seg_off[r.seg] + row0;
-          auto stage = [&](const uint32_t(&v)[32], int j) {
-            uint8_t* buf = open_block();
-#pragma unroll
-            for (int i = 0; i < 32; ++i) *cell(buf, i) = to_bf16(__uint_as_float(v[i]));
-            close_tokens(buf, &P.mo, P.out, row + j * 32, ch0, P.M, 32, rows - j * 32, nc);
-          };
-          for (int j = half; j < nchunks; j += 4) {
-            uint32_t v0[32], v1[32];
-            tmem_ld32(d + j * 32, v0);
-            if (j + 2 < nchunks) tmem_ld32(d + j * 32 + 64, v1);
-            tmem_ld_wait();
-            stage(v0, j);
-            if (j + 2 < nchunks) stage(v1, j + 2);
-          }
         } else {
-          const int ch = ch0 + lane;
-          const bool up_half = GATED && q >= 2;
-          float b0 = 0.0f;
-          if (P.bias != nullptr && ch < P.M)
-            b0 = __ldg(P.bias + (size_t)r.e * P.M * (GATED ? 2 : 1) + (up_half ? P.M : 0) + ch);
           const int64_t row = (int64_t)seg_off[r.seg] + row0;
+          const bool up_half = GATED && q >= 2;
+          // this thread's channels: ch0 + lane/4 + 8c
+          float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+          if (MODE == kFwd && P.bias != nullptr) {
+            const float* bp = P.bias + (size_t)r.e * P.M * (GATED ? 2 : 1) + (up_half ? P.M : 0) + ch0;
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+              const int ch = (lane >> 2) + 8 * c;
+              if (ch < nc) bias[c] = __ldg(bp + ch);
+            }
+          }
+          uint32_t next[32];
+          if (half < nchunks) load_block(d + half * 32, next);
           for (int j = half; j < nchunks; j += 2) {
             const int64_t row_j = row + j * 32;
             const int nr = rows - j * 32;
@@ -687,45 +687,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             const int tok0 = up_half ? 16 : 0;
             constexpr int kTok = GATED ? 16 : 32;
             // the residual's block, on its way while the accumulator is read
-            uint4 res[kTok / 8];
-            if (P.residual != nullptr) {
-              const uint16_t* src = P.residual + (row_j + tok0) * P.M + ch0;
+            uint4 res[MODE == kFwd ? kTok / 8 : 1];
+            if constexpr (MODE == kFwd) {
+              if (P.residual != nullptr) {
+                const uint16_t* src = P.residual + (row_j + tok0) * P.M + ch0;
 #pragma unroll
-              for (int i = 0; i < kTok / 8; ++i) {
-                const int rr = i * 8 + frow;
-                res[i] = rr + tok0 < nr && fcol < nc
-                             ? *reinterpret_cast<const uint4*>(src + (size_t)rr * P.M + fcol)
-                             : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < kTok / 8; ++i) {
+                  const int rr = i * 8 + frow;
+                  res[i] = rr + tok0 < nr && fcol < nc
+                               ? *reinterpret_cast<const uint4*>(src + (size_t)rr * P.M + fcol)
+                               : make_uint4(0, 0, 0, 0);
+                }
               }
             }
-            uint32_t v[32];
-            tmem_ld32(d + j * 32, v);
-            tmem_ld_wait();
-            // this lane holds one channel of 32 tokens: staged token-major
+            tmem_ld_wait(next);
             float z[32];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) z[i] = __uint_as_float(v[i]) + b0;
-            if (P.pre != nullptr) {
-              const int wide = P.M * (GATED ? 2 : 1);
-              uint8_t* buf = open_block();
+            for (int i = 0; i < 32; ++i)
+              z[i] = __uint_as_float(next[i]) + bias[(i >> 4) * 2 + ((i >> 1) & 1)];
+            if (j + 2 < nchunks) load_block(d + (j + 2) * 32, next);
+            if constexpr (MODE == kFwd) {
+              if (P.pre != nullptr) {
+                const int wide = P.M * (GATED ? 2 : 1);
+                uint8_t* buf = open_block();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) *cell(buf, i) = to_bf16(z[i]);
-              // (a gate half's block may reach into the up half's columns: lane stores)
-              const bool inside = !GATED || up_half || nc >= 32;
-              close_tokens(buf, &P.mp, P.pre, row_j, (up_half ? P.M : 0) + ch0, wide,
-                           inside ? 32 : INT_MAX, nr, nc);
+                for (int i = 0; i < 4; ++i) stage8(buf, i, z, i, 4);
+                // (a gate half's block may reach into the up half's columns: lane stores)
+                const bool inside = !GATED || up_half || nc >= 32;
+                close_tokens(buf, &P.mp, P.pre, row_j, (up_half ? P.M : 0) + ch0, wide,
+                             inside ? 32 : INT_MAX, nr, nc);
+              }
             }
+            float y[kTok];  // the results: fragments of kTok / 8 token groups
             if constexpr (GATED) {
               // lanes 0..63 of the accumulator are gates, 64..127 the same channels' ups.
               // The gate's warp takes tokens 0..15, the up's 16..31: each hands the other
-              // its 16 values through a staging block, in fp32.
+              // its 16 values a thread through a staging block, in fp32.
               uint64_t* bar = &swap[half * 2 + (q & 1)];
               uint8_t* buf = open_block();
-              float* mine = reinterpret_cast<float*>(buf);
-              const float* theirs =
-                  reinterpret_cast<const float*>(epi + ((wid - 4) ^ 2) * 4096 + (buf - blocks));
+              float4* mine = reinterpret_cast<float4*>(buf) + lane;
+              const float4* theirs =
+                  reinterpret_cast<const float4*>(epi + ((wid - 4) ^ 2) * 4096 + (buf - blocks)) + lane;
 #pragma unroll
-              for (int i = 0; i < 16; ++i) mine[i * 32 + lane] = up_half ? z[i] : z[16 + i];
+              for (int i = 0; i < 4; ++i) {  // (h, j) = (i / 2, i % 2 of the pair handed over)
+                const int lo = (i >> 1) * 16 + (i & 1) * 4, hi = lo + 8;
+                mine[i * 32] = up_half ? make_float4(z[lo], z[lo + 1], z[lo + 2], z[lo + 3])
+                                       : make_float4(z[hi], z[hi + 1], z[hi + 2], z[hi + 3]);
+              }
               __syncwarp();
               if (elect_one()) {
                 bulk_commit();
@@ -735,9 +743,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 ok = false;
                 break;
               }
-              float other[16];
+              float4 other[4];
 #pragma unroll
-              for (int i = 0; i < 16; ++i) other[i] = theirs[i * 32 + lane];
+              for (int i = 0; i < 4; ++i) other[i] = theirs[i * 32];
               __syncwarp();
               if (lane == 0) mbar_arrive(bar);
               if (!warp_wait(bar, nswap++ & 1u)) {
@@ -745,31 +753,54 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                 break;
               }
 #pragma unroll
-              for (int i = 0; i < 16; ++i) {
-                const float g = up_half ? other[i] : z[i], u = up_half ? z[16 + i] : other[i];
-                z[i] = g * sigmoid_f(g) * u;
+              for (int i = 0; i < 4; ++i) {
+                const int lo = (i >> 1) * 16 + (i & 1) * 4, hi = lo + 8;
+                const float o[4] = {other[i].x, other[i].y, other[i].z, other[i].w};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                  const float g = up_half ? o[u] : z[lo + u], v = up_half ? z[hi + u] : o[u];
+                  y[i * 4 + u] = g * sigmoid_f(g) * v;
+                }
               }
-            } else if (P.act == MOE_ACT_RELU) {
+            } else {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) z[i] = z[i] < 0.0f ? 0.0f : z[i];
-            } else if (P.act == MOE_ACT_GELU) {
+              for (int i = 0; i < 32; ++i) y[i] = z[i];
+              if (MODE == kFwd) {
+                if (P.act == MOE_ACT_RELU) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) z[i] = gelu_f(z[i]);
-            } else if (P.act == MOE_ACT_SILU) {
+                  for (int i = 0; i < 32; ++i) y[i] = z[i] < 0.0f ? 0.0f : z[i];
+                } else if (P.act == MOE_ACT_GELU) {
 #pragma unroll
-              for (int i = 0; i < 32; ++i) z[i] = z[i] * sigmoid_f(z[i]);
+                  for (int i = 0; i < 32; ++i) y[i] = gelu_f(z[i]);
+                } else if (P.act == MOE_ACT_SILU) {
+#pragma unroll
+                  for (int i = 0; i < 32; ++i) y[i] = z[i] * sigmoid_f(z[i]);
+                }
+              }
             }
             uint8_t* buf = open_block();
-            if (P.residual != nullptr) {
-              // through the staging block to this lane's column; added in fp32
+            if constexpr (MODE == kFwd) {
+              if (P.residual != nullptr) {
+                // through the staging block into the fragments; added in fp32
 #pragma unroll
-              for (int i = 0; i < kTok / 8; ++i) *piece(buf, i * 8 + frow) = res[i];
-              __syncwarp();
+                for (int i = 0; i < kTok / 8; ++i) *piece(buf, i * 8 + frow) = res[i];
+                __syncwarp();
 #pragma unroll
-              for (int i = 0; i < kTok; ++i) z[i] += bf16lo(*cell(buf, i));
+                for (int i = 0; i < kTok / 8; ++i) {
+                  uint32_t f[4];
+                  ldmatrix_t(smem_addr(buf) + t_addr + i * 512, f);
+#pragma unroll
+                  for (int c = 0; c < 4; ++c) {
+                    float* at = y + (c >> 1) * (kTok / 2) + 4 * i + (c & 1) * 2;
+                    at[0] += bf16lo(f[c]);
+                    at[1] += bf16hi(f[c]);
+                  }
+                }
+                __syncwarp();
+              }
             }
 #pragma unroll
-            for (int i = 0; i < kTok; ++i) *cell(buf, i) = to_bf16(z[i]);
+            for (int i = 0; i < kTok / 8; ++i) stage8(buf, i, y, i, kTok / 8);
             close_tokens(buf, &P.mo, P.out, row_j + tok0, ch0, P.M, kTok, nr - tok0, nc);
           }
         }
@@ -870,7 +901,7 @@ cudaError_t token_operand(GemmParams& P, const ExpertMatmul& a, const void* rows
   }
   P.kdim = cols;
   P.band = 8;
-  P.max_n = 512;
+  P.max_n = 256;
   // ranking costs E^2 / 384 steps a CTA: where tiles are large enough to differ
   P.sorted = a.E > 1 && a.assignments >= (int64_t)32 * a.E;
   return cudaSuccess;
