@@ -43,7 +43,8 @@ constexpr int kABytes = kBM * kBK * 2;
 constexpr int kSlots = 8;     // slices in flight, at most (a power of two)
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = (4 + kEpiWarps) * 32;
-constexpr int kEpiBytes = kEpiWarps * 2 * 2048;  // two 32 x 32 bf16 blocks a warp
+// Staging: two 32 x 32 bf16 blocks a warp; weights gradient one of 32 x 128.
+constexpr int epi_bytes(bool weights) { return kEpiWarps * (weights ? 8192 : 4096); }
 constexpr int kMaxSlice = kABytes + 2 * 128 * kBK * 2;
 constexpr int kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
@@ -172,7 +173,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* epi = smem + P.ring;
-  int32_t* seg_off = reinterpret_cast<int32_t*>(epi + kEpiBytes);
+  int32_t* seg_off = reinterpret_cast<int32_t*>(epi + epi_bytes(MODE == kWeights));
   int32_t* seg_rows = seg_off + P.E;
   // forward / rows: exclusive prefix of token tiles [E+1], and the experts in the
   // table's order [E]
@@ -360,10 +361,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   // Steps wholly behind it are skipped; in the last step they become zero in
   // both operands (zero times NaN is not zero).  One warp, on this CTA's half.
   auto zero_stale = [&](uint8_t* slice, int depth, int k0, int blocks) {
-    const int valid = depth - k0, stale = 16 - (valid & 15);
-    for (int i = lane; i < blocks * stale * 8; i += 32) {
-      const int q = i & 7, row = valid + (i >> 3) % stale, blk = (i >> 3) / stale;
-      *reinterpret_cast<uint4*>(slice + blk * 8192 + row * 128 + q * 16) = make_uint4(0, 0, 0, 0);
+    const int valid = depth - k0, end = (valid + 15) & ~15;
+    for (int row = valid + (lane >> 3); row < end; row += 4) {
+      uint8_t* at = slice + row * 128 + (lane & 7) * 16;
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (b < blocks) *reinterpret_cast<uint4*>(at + b * 8192) = make_uint4(0, 0, 0, 0);
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -632,39 +635,46 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const int rows = min(r.n, r.row0 + r.rows - row0);
         const int nchunks = (rows + 31) >> 5;
         if constexpr (MODE == kWeights) {
-          // this lane holds 32 columns of one row of dW; two blocks at a time
-          auto stage = [&](const uint32_t(&v)[32], int j) {
-            uint8_t* buf = open_block();
+          // Warps 4..7 take columns 0..127, warps 8..11 the others, 64 at a time.  A lane
+          // holds 32 columns of one row of dW; 32 rows of 128 bytes (16-byte pieces
+          // swizzled by the row) are staged in one of two 4 KiB blocks and stored as one
+          // box while the other block is filled.  (Boxes of 32 x 32 held the gradient of
+          // 256-row experts at 3.2 TB/s, one block of 8 KiB at 3.7.)
+          const int col0 = half * 128, ncols = min(128, rows - col0);
+          uint32_t v[32];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              uint32_t w[4];
+          for (int i = 0; i < 32; ++i) v[i] = 0u;
+          if (!empty_sum && ncols > 0) tmem_ld32(d + col0, v);
 #pragma unroll
-              for (int u = 0; u < 4; ++u)
-                w[u] = pack2(__uint_as_float(v[8 * i + 2 * u]), __uint_as_float(v[8 * i + 2 * u + 1]));
-              *reinterpret_cast<uint4*>(buf + lane * 64 + ((i ^ ((lane >> 1) & 3)) << 4)) =
-                  make_uint4(w[0], w[1], w[2], w[3]);
-            }
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (elect_one()) {
-              if (nc > 0) tma_store_3d(&P.mo, buf, row0 + j * 32, ch0, r.e);
-              bulk_commit();
-            }
-          };
-          for (int j = half; j < nchunks; j += 4) {
-            uint32_t v0[32], v1[32];
-            if (!empty_sum) {
-              tmem_ld32(d + j * 32, v0);
-              if (j + 2 < nchunks) tmem_ld32(d + j * 32 + 64, v1);
-              tmem_ld_wait(v0);
-              tmem_ld_wait(v1);
-            } else {
+          for (int j = 0; j < 4; ++j) {
+            if (j * 32 < ncols) {
+              uint8_t* buf = epi + (wid - 4) * 8192 + (j >> 1) * 4096;
+              if ((j & 1) == 0) {
+                if (elect_one()) bulk_wait_read<1>();
+                __syncwarp();
+              }
+              uint32_t w[16];
+              if (!empty_sum) tmem_ld_wait(v);
 #pragma unroll
-              for (int i = 0; i < 32; ++i) v0[i] = v1[i] = 0u;
+              for (int i = 0; i < 16; ++i)
+                w[i] = pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+              if (!empty_sum && (j + 1) * 32 < ncols) tmem_ld32(d + col0 + (j + 1) * 32, v);
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                *reinterpret_cast<uint4*>(buf + lane * 128 + ((((j & 1) * 4 + i) ^ (lane & 7)) << 4)) =
+                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+              if ((j & 1) != 0 || (j + 1) * 32 >= ncols) {
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (elect_one()) {
+                  if (nc > 0) tma_store_3d(&P.mo, buf, row0 + col0 + (j >> 1) * 64, ch0, r.e);
+                  bulk_commit();
+                }
+              }
             }
-            stage(v0, j);
-            if (j + 2 < nchunks) stage(v1, j + 2);
           }
+          // (both blocks take turns: a tile that ends after the first gives the second's turn)
+          if (ncols <= 64 && elect_one()) bulk_commit();
         } else {
           const int64_t row = (int64_t)seg_off[r.seg] + row0;
           const bool up_half = GATED && q >= 2;
@@ -865,9 +875,10 @@ template <int MODE, bool GATED>
 cudaError_t launch_gemm(const LaunchEnv& env, GemmParams& P, int64_t max_tiles) {
   const size_t table = sizeof(int32_t) * ((size_t)P.E * (MODE == kWeights ? 2 : 4) + 1);
   const size_t smem = kSmemLimit - kSmemStatic;
-  P.ring = (int)((smem - 1024 - kEpiBytes - table) / 1024 * 1024);
-  static_assert(kSmemLimit - kSmemStatic - 1024 - kEpiBytes - 16 * 1024 - 1024 >= 3 * kMaxSlice,
-                "three of the largest slices");
+  P.ring = (int)((smem - 1024 - epi_bytes(MODE == kWeights) - table) / 1024 * 1024);
+  static_assert(kSmemLimit - kSmemStatic - 1024 - epi_bytes(false) - 17 * 1024 >= 3 * kMaxSlice &&
+                    kSmemLimit - kSmemStatic - 1024 - epi_bytes(true) - 9 * 1024 >= 4 * 32 * 1024,
+                "three of the largest slices, four of the weights gradient's");
   int per_sm = 1;
   const auto kernel = expert_gemm_kernel<MODE, GATED>;
   cudaError_t err = blocks_per_sm((const void*)kernel, kGemmThreads, smem, &per_sm);
@@ -962,7 +973,7 @@ cudaError_t launch_expert_grad_weights(const LaunchEnv& env, const ExpertMatmul&
   segments_of(P, a);
   cudaError_t err = make_map(&P.ma, dz, wide, a.N, 0, 64, kBK);
   if (err == cudaSuccess) err = make_map(&P.mb[0], a.x, a.in_features, a.N, 0, 64, kBK);
-  if (err == cudaSuccess) err = make_map(&P.mo, grad_w, a.in_features, wide, a.E, 32, 32);
+  if (err == cudaSuccess) err = make_map(&P.mo, grad_w, a.in_features, wide, a.E, 64, 32);
   if (err != cudaSuccess) return err;
   P.out = static_cast<uint16_t*>(grad_w);
   P.M = wide;
