@@ -32,7 +32,7 @@ struct ActParams {
   const int32_t* off;
   WsHeader* hdr;
   int64_t N, max_rows;
-  int E, capacity, F, W, act;
+  int E, capacity, F, W;
 };
 
 __device__ __forceinline__ int seg_rows(const ActParams& P, int e, int* off) {
@@ -51,18 +51,31 @@ __device__ __forceinline__ int seg_rows(const ActParams& P, int e, int* off) {
   return r;
 }
 
-// d z for one channel: slope of the activation (swiglu: of the gate half).
-__device__ __forceinline__ float slope(float z, int act) {
-  switch (act) {
-    case MOE_ACT_RELU: return z > 0.0f ? 1.0f : 0.0f;
-    case MOE_ACT_GELU:
-      return 0.5f * (1.0f + erff(z * 0.70710678118654752f)) +
-             z * expf(-0.5f * z * z) * 0.39894228040143268f;
-    case MOE_ACT_SILU:
-    case MOE_ACT_SWIGLU: {
-      const float s = 1.0f / (1.0f + expf(-z));
-      return s * (1.0f + z * (1.0f - s));
-    }
+// Sigmoid by the fast exponential and quotient (a few units in the last place;
+// the full-precision forms made this kernel three times as long, bound by issue).
+__device__ __forceinline__ float sigmoid_f(float z) {
+  return __fdividef(1.0f, 1.0f + __expf(-z));
+}
+
+// Slope of the activation at z.  gelu: Phi(z) + z phi(z), Phi's tail by the
+// rational approximation 7.1.26 of Abramowitz and Stegun's Handbook (as in the
+// forward product), which shares the exponential with phi.
+template <int ACT>
+__device__ __forceinline__ float slope(float z) {
+  if (ACT == MOE_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
+  if (ACT == MOE_ACT_GELU) {
+    const float x = fabsf(z) * 0.70710678f, e = __expf(-x * x);
+    const float t = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+    float q = fmaf(1.061405429f, t, -1.453152027f);
+    q = fmaf(q, t, 1.421413741f);
+    q = fmaf(q, t, -0.284496736f);
+    q = fmaf(q, t, 0.254829592f);
+    const float tail = 0.5f * q * t * e;
+    return fmaf(z * 0.39894228f, e, z < 0.0f ? tail : 1.0f - tail);
+  }
+  if (ACT == MOE_ACT_SILU || ACT == MOE_ACT_SWIGLU) {
+    const float s = sigmoid_f(z);
+    return s * fmaf(z, 1.0f - s, 1.0f);
   }
   return 1.0f;
 }
@@ -83,6 +96,9 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
   return make_uint4(w[0], w[1], w[2], w[3]);
 }
 
+constexpr int kUnroll = 2;  // rows of a warp whose loads are in flight together
+
+template <int ACT>
 __global__ void __launch_bounds__(kThreads)
     expert_act_backward_kernel(ActParams P) {
   extern __shared__ int32_t tab[];
@@ -118,7 +134,7 @@ __global__ void __launch_bounds__(kThreads)
   }
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int strips = (P.F + 255) / 256;  // 256 channels: 8 a lane
-  const bool gated = P.act == MOE_ACT_SWIGLU;
+  constexpr bool gated = ACT == MOE_ACT_SWIGLU, plain = ACT == MOE_ACT_NONE;
   for (int64_t u = blockIdx.x; u < (int64_t)tiles * strips; u += gridDim.x) {
     const int tile = (int)(u / strips), strip = (int)(u - (int64_t)tile * strips);
     int lo = 0, hi = P.E;
@@ -136,33 +152,47 @@ __global__ void __launch_bounds__(kThreads)
 #pragma unroll
     for (int i = 0; i < 8; ++i) s0[i] = s1[i] = 0.0f;
     if (c < P.F) {
-      for (int r = w; r < n; r += kWarps) {
-        const size_t p = (size_t)off[lo] + r0 + r;
-        float d[8], z[8];
-        unpack8(ld16_stream(P.dy + p * P.F + c), d);
-        if (gated) {
-          float up[8], g[8];
-          unpack8(ld16_stream(P.z + p * P.W + c), z);
-          unpack8(ld16_stream(P.z + p * P.W + P.F + c), up);
+      for (int r = w; r < n; r += kUnroll * kWarps) {
+        uint4 dv[kUnroll], zv[kUnroll], uv[kUnroll];
 #pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float s = 1.0f / (1.0f + expf(-z[i]));
-            g[i] = d[i] * up[i] * (s * (1.0f + z[i] * (1.0f - s)));
-            up[i] = d[i] * (z[i] * s);
-            s0[i] += g[i];
-            s1[i] += up[i];
+        for (int k = 0; k < kUnroll; ++k) {
+          if (r + k * kWarps < n) {
+            const size_t p = (size_t)off[lo] + r0 + r + k * kWarps;
+            dv[k] = ld16_stream(P.dy + p * P.F + c);
+            if (!plain) zv[k] = ld16_stream(P.z + p * P.W + c);
+            if (gated) uv[k] = ld16_stream(P.z + p * P.W + P.F + c);
           }
-          st16(P.dz + p * P.W + c, pack8(g));
-          st16(P.dz + p * P.W + P.F + c, pack8(up));
-        } else {
-          if (P.act != MOE_ACT_NONE) {
-            unpack8(ld16_stream(P.z + p * P.W + c), z);
+        }
 #pragma unroll
-            for (int i = 0; i < 8; ++i) d[i] *= slope(z[i], P.act);
-            st16(P.dz + p * P.W + c, pack8(d));
+        for (int k = 0; k < kUnroll; ++k) {
+          if (r + k * kWarps < n) {
+            const size_t p = (size_t)off[lo] + r0 + r + k * kWarps;
+            float d[8], z[8];
+            unpack8(dv[k], d);
+            if (!plain) unpack8(zv[k], z);
+            if (gated) {
+              float up[8], g[8];
+              unpack8(uv[k], up);
+#pragma unroll
+              for (int i = 0; i < 8; ++i) {
+                const float s = sigmoid_f(z[i]);
+                g[i] = d[i] * up[i] * (s * fmaf(z[i], 1.0f - s, 1.0f));
+                up[i] = d[i] * (z[i] * s);
+                s0[i] += g[i];
+                s1[i] += up[i];
+              }
+              st16(P.dz + p * P.W + c, pack8(g));
+              st16(P.dz + p * P.W + P.F + c, pack8(up));
+            } else {
+              if (!plain) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) d[i] *= slope<ACT>(z[i]);
+                st16(P.dz + p * P.W + c, pack8(d));
+              }
+#pragma unroll
+              for (int i = 0; i < 8; ++i) s0[i] += d[i];
+            }
           }
-#pragma unroll
-          for (int i = 0; i < 8; ++i) s0[i] += d[i];
         }
       }
     }
@@ -262,16 +292,22 @@ cudaError_t launch_expert_act_backward(const LaunchEnv& env, const ExpertMatmul&
   P.capacity = a.capacity;
   P.F = a.out_features;
   P.W = a.act == MOE_ACT_SWIGLU ? 2 * a.out_features : a.out_features;
-  P.act = a.act;
   const size_t smem = sizeof(int32_t) * (3 * (size_t)P.E + 1);
   int per_sm = 1;
-  cudaError_t err = blocks_per_sm((const void*)expert_act_backward_kernel, kThreads, smem, &per_sm);
+  void (*kernel)(ActParams) = expert_act_backward_kernel<MOE_ACT_NONE>;
+  switch (a.act) {
+    case MOE_ACT_RELU: kernel = expert_act_backward_kernel<MOE_ACT_RELU>; break;
+    case MOE_ACT_GELU: kernel = expert_act_backward_kernel<MOE_ACT_GELU>; break;
+    case MOE_ACT_SILU: kernel = expert_act_backward_kernel<MOE_ACT_SILU>; break;
+    case MOE_ACT_SWIGLU: kernel = expert_act_backward_kernel<MOE_ACT_SWIGLU>; break;
+  }
+  cudaError_t err = blocks_per_sm((const void*)kernel, kThreads, smem, &per_sm);
   if (err != cudaSuccess) return err;
   const int64_t strips = (P.F + 255) / 256;
   int64_t grid = expert_act_tiles(a.assignments, a.E) * strips;
   if (grid > (int64_t)per_sm * env.num_sms) grid = (int64_t)per_sm * env.num_sms;
   if (grid < 1) grid = 1;
-  err = launch_pdl(env, expert_act_backward_kernel, dim3((unsigned)grid), dim3(kThreads), smem, P);
+  err = launch_pdl(env, kernel, dim3((unsigned)grid), dim3(kThreads), smem, P);
   if (err != cudaSuccess || grad_bias == nullptr) return err;
   return launch_pdl(env, expert_bias_reduce_kernel, dim3((unsigned)((P.W + 31) / 32), (unsigned)P.E),
                     dim3(kThreads), 0, P, grad_bias);

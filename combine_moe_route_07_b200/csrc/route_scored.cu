@@ -11,11 +11,24 @@
 //
 // Scores and keys are defined in binary64: a selection is a discontinuous
 // function of the keys, so two evaluations agree only if neither rounds keys
-// that differ onto one value.
+// that differ onto one value.  A binary64 score of every expert is what bounds
+// that definition taken literally (Fine-grained, 65536 x 512: 504 us), so the
+// keys of a token are formed in binary32 with a bound on their error, and
+// binary64 decides among the few that the bound leaves open:
+//   1. group scores in binary32; the kept groups are certain when the gap
+//      between the last kept and the first left out exceeds the bound;
+//   2. tau = the k-th largest lane maximum of the kept keys, less the bound: no
+//      key below it can be among the k best; the keys at or above it (k to k+4
+//      of them, usually) are compacted, one a lane;
+//   3. their binary64 keys are ranked against each other, ties by expert.
+// A token whose groups or candidates stay open (ties, masks that leave less
+// than k finite keys, NaN, more than 32 candidates) is decided in binary64
+// throughout, out of line.
 #include <math.h>
 
 #include "common.cuh"
 #include "kernels.h"
+#include "route_core.cuh"
 
 namespace moe {
 
@@ -138,11 +151,218 @@ __device__ bool scored_token_exact(const float* __restrict__ row, const float* _
 __device__ __forceinline__ float scored_gate(double s, int renorm, double scale) {
   if (renorm) {
     const double sum = wsum_d(s);
-    s = sum > 0.0 ? s / sum : 0.0;
+    s = sum > 1e-290 ? s * __drcp_rn(sum) : sum > 0.0 ? s / sum : 0.0;
   }
   return (float)(s * scale);
 }
 
+// Per-warp shared memory: E doubles (the exact form's keys; the binary32 keys
+// while groups are scored), then the candidates.
+constexpr int kCand = 32;
+struct CandArea {
+  double key[kCand], score[kCand];
+  int expert[kCand];
+  int slot[kCand];
+};
+
+__device__ __noinline__ bool scored_token_slow(const float* row, const float* bias, int E, int k,
+                                               const ScoreRule& R, int lane, double* key,
+                                               int& sel_e, double& sel_s) {
+  return scored_token_exact(row, bias, E, k, R, lane, key, sel_e, sel_s);
+}
+
+__device__ __forceinline__ float redux_max_f(float v) { return warp_max_nan(v); }
+
+// One token, decided as above; false: not decided.  Lane j < k returns slot j's
+// expert and score.  `skey` holds E floats.
+template <int NK, bool SOFTMAX, bool BIAS>
+__device__ __forceinline__ bool scored_token_fast(const float* __restrict__ row, int E, int k,
+                                                  const ScoreRule& R, int lane, uint32_t vmask,
+                                                  const float (&bias)[BIAS ? NK : 1],
+                                                  const float* __restrict__ gbias, float* skey,
+                                                  CandArea* C, int& sel_e, double& sel_s) {
+  float key[NK];
+#pragma unroll
+  for (int i = 0; i < NK; ++i) key[i] = ((vmask >> i) & 1u) ? __ldg(row + lane + 32 * i) : -INFINITY;
+  float m = 0.0f, sum = 1.0f;
+  const bool grouped = R.top_groups < R.groups;
+  // without a bias the logits are in the softmax's order (but their sums are not)
+  const bool raw = SOFTMAX && !BIAS && !(grouped && R.group_top == 2);
+  if (SOFTMAX) {
+    m = key[0];
+#pragma unroll
+    for (int i = 1; i < NK; ++i) m = max2_nan(m, key[i]);
+    m = redux_max_f(m);
+    if (!(fabsf(m) < INFINITY)) return false;  // NaN, or a row without a finite maximum
+    if (!raw || !R.renorm) {
+      float part = 0.0f;
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        const float p = __expf(key[i] - m);
+        part += p;
+        if (!raw) key[i] = p;
+      }
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kFull, part, o);
+      sum = part;
+    }
+    if (BIAS) {
+      const float inv = __fdividef(1.0f, sum);
+#pragma unroll
+      for (int i = 0; i < NK; ++i) key[i] = ((vmask >> i) & 1u) ? fmaf(key[i], inv, bias[i]) : -INFINITY;
+    } else if (!raw) {  // (unnormalised: the scores' order and that of their sums)
+#pragma unroll
+      for (int i = 0; i < NK; ++i) key[i] = ((vmask >> i) & 1u) ? key[i] : -INFINITY;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const float s = __fdividef(1.0f, 1.0f + __expf(-key[i]));
+      key[i] = ((vmask >> i) & 1u) ? (BIAS ? s + bias[i] : s) : -INFINITY;
+    }
+  }
+  // How far a key can be from its binary64 value: scores are within 2^-21 of theirs
+  // (the fast exponential is off by 2^-22 and its argument's rounding, which the
+  // scores damp; quotient 2^-22; sum of the softmax 2^-22), one addition 2^-24 of the
+  // key.  Logits are exact; two of them closer than 2^-20 of their size are left to
+  // binary64, whose exponentials could coincide.
+  auto bound = [&](float v) { return 1.0e-6f + 2.5e-7f * (fabsf(v) + (raw ? fabsf(m) : 0.0f)); };
+
+  if (grouped) {
+    // Lg lanes a group; they walk its experts in turns that keep the groups' lanes on
+    // different banks, and meet in a butterfly of (largest, second largest).
+    const int G = E / R.groups;
+    const int Lg = 1 << (31 - __clz(32 / R.groups));
+    const int g = lane / Lg, sub = lane & (Lg - 1);
+    const int steps = (G + Lg - 1) / Lg;
+#pragma unroll
+    for (int i = 0; i < NK; ++i)
+      if ((vmask >> i) & 1u) skey[lane + 32 * i] = key[i];
+    __syncwarp();
+    float a = -INFINITY, b = -INFINITY;
+    bool odd = false;
+    if (g < R.groups) {
+      int turn = g < steps ? g : g % steps;
+      for (int it = 0; it < steps; ++it) {
+        const int at = sub + Lg * turn;
+        turn = turn + 1 == steps ? 0 : turn + 1;
+        if (at < G) {
+          const float v = skey[g * G + at];
+          odd |= !(v < INFINITY);
+          b = fmaxf(b, fminf(a, v));
+          a = fmaxf(a, v);
+        }
+      }
+    }
+    if (__any_sync(kFull, odd)) return false;
+    for (int o = 1; o < Lg; o <<= 1) {
+      const float oa = __shfl_xor_sync(kFull, a, o), ob = __shfl_xor_sync(kFull, b, o);
+      b = fmaxf(fminf(a, oa), fmaxf(b, ob));
+      a = fmaxf(a, oa);
+    }
+    float score = R.group_top == 2 ? a + b : a;
+    if (g >= R.groups || sub != 0) score = -INFINITY;
+    // the largest key among those that scores are made of (a group without a finite
+    // key scores -inf in any precision)
+    const float mag = score == -INFINITY ? 0.0f : fmaxf(fabsf(a), R.group_top == 2 ? fabsf(b) : 0.0f);
+    const float big = redux_max_f(mag);
+    uint32_t kept = 0u;
+    float last = 0.0f;
+    for (int r = 0; r < R.top_groups; ++r) {
+      last = redux_max_f(score);
+      const unsigned hold = __ballot_sync(kFull, score == last);
+      const int who = __ffs(hold) - 1;
+      kept |= 1u << (who / Lg);
+      if (lane == who) score = -INFINITY;
+    }
+    const float next = redux_max_f(score);
+    if (!(last - next > 4.0f * bound(big))) return false;
+    const uint32_t magic = G > 1 ? (uint32_t)((0x100000000ull + (uint64_t)G - 1) / (uint64_t)G) : 0u;
+#pragma unroll
+    for (int i = 0; i < NK; ++i) {
+      const uint32_t e = (uint32_t)(lane + 32 * i);
+      const uint32_t q = G > 1 ? __umulhi(e, magic) : e;
+      if (!((kept >> (q & 31u)) & 1u)) key[i] = -INFINITY;
+    }
+  }
+
+  // tau: the k-th largest lane maximum, on order codes whose low 5 bits are the lane
+  float mm = key[0];
+#pragma unroll
+  for (int i = 1; i + 1 < NK; i += 2) mm = max3_nan(mm, key[i], key[i + 1]);
+  mm = max2_nan(mm, key[NK - 1]);
+  const float wmax = redux_max_f(mm);
+  if (!(wmax < INFINITY)) return false;
+  uint32_t code = (order_code(mm) & ~31u) | (uint32_t)(31 - lane);
+  uint32_t top = 0u;
+#pragma unroll 1
+  for (int j = 0; j < k; ++j) {
+    top = __reduce_max_sync(kFull, code);
+    code = code == top ? 0u : code;
+  }
+  if (top < 0x00800000u) return false;  // a lane without a finite key among the k
+  const float tau = code_float(top & ~31u);
+  if (raw && !(tau - m > -700.0f)) return false;  // scores that vanish in binary64 tie
+  const float open = 2.0f * bound(fmaxf(fabsf(tau), BIAS ? fabsf(wmax) : 0.0f));
+  const float thr = tau - open;
+  uint32_t cm = 0u;
+#pragma unroll
+  for (int i = 0; i < NK; ++i) cm |= (key[i] >= thr) ? (1u << i) : 0u;
+  const int total = (int)__reduce_add_sync(kFull, (unsigned)__popc(cm));
+  if (total > kCand || total < k) return false;
+  int base = 0;
+#pragma unroll 1
+  while (true) {
+    const unsigned any = __ballot_sync(kFull, cm != 0u);
+    if (any == 0u) break;
+    if (cm != 0u) {
+      C->expert[base + __popc(any & lanemask_lt())] = lane + 32 * (__ffs(cm) - 1);
+      cm &= cm - 1u;
+    }
+    base += __popc(any);
+  }
+  __syncwarp();
+  int e = 0;
+  double v = 0.0, s = 0.0;
+  if (lane < total) {
+    e = C->expert[lane];
+    const double l = (double)__ldg(row + e);
+    if (SOFTMAX) {
+      s = exp(l - (double)m);
+      if (BIAS || !R.renorm) s /= (double)sum;
+    } else {
+      s = 1.0 / (1.0 + exp(-l));
+    }
+    v = BIAS ? s + (double)__ldg(gbias + e) : s;
+    C->key[lane] = v;
+  }
+  __syncwarp();
+  int n = 0;
+  if (lane < total)
+    for (int j = 0; j < total; ++j) {
+      const double o = C->key[j];
+      n += (o > v || (o == v && C->expert[j] < e)) ? 1 : 0;
+    }
+  __syncwarp();
+  if (lane < total) {
+    C->slot[n] = e;
+    C->score[n] = s;
+    C->key[n] = v;
+  }
+  __syncwarp();
+  if (SOFTMAX && BIAS) {
+    // the sum of the exponentials is a binary32 one here: neighbours closer than its
+    // error are left open
+    const bool close = lane < k && lane + 1 < total && !(C->key[lane] - C->key[lane + 1] > (double)open);
+    if (__any_sync(kFull, close)) return false;
+  }
+  sel_e = lane < k ? C->slot[lane] : 0;
+  sel_s = lane < k ? C->score[lane] : 0.0;
+  __syncwarp();
+  return true;
+}
+
+template <int NK, bool SOFTMAX, bool BIAS>
 __global__ void __launch_bounds__(kScoredWarps * 32)
     route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ bias, int T,
                         int E, int k, ScoreRule R, int32_t* __restrict__ ids,
@@ -152,10 +372,26 @@ __global__ void __launch_bounds__(kScoredWarps * 32)
   pdl_trigger();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   double* key = skey + (size_t)w * E;
+  CandArea* C = reinterpret_cast<CandArea*>(skey + (size_t)kScoredWarps * E) + w;
+  uint32_t vmask = 0u;
+  float b[BIAS ? NK : 1];
+#pragma unroll
+  for (int i = 0; i < NK; ++i) {
+    const int e = lane + 32 * i;
+    if (e < E) vmask |= 1u << i;
+    if (BIAS) b[i] = e < E ? __ldg(bias + e) : 0.0f;
+  }
+  const bool fast = R.groups <= 32 || R.top_groups == R.groups;
   for (int t = blockIdx.x * kScoredWarps + w; t < T; t += gridDim.x * kScoredWarps) {
+    const float* row = logits + (size_t)t * E;
     int e = 0;
     double s = 0.0;
-    const bool ok = scored_token_exact(logits + (size_t)t * E, bias, E, k, R, lane, key, e, s);
+    bool ok = fast && scored_token_fast<NK, SOFTMAX, BIAS>(row, E, k, R, lane, vmask, b, bias,
+                                                           reinterpret_cast<float*>(key), C, e, s);
+    if (!ok) {
+      __syncwarp();
+      ok = scored_token_slow(row, bias, E, k, R, lane, key, e, s);
+    }
     float g = 0.0f;
     if (ok) {
       g = scored_gate(s, R.renorm, R.scale);
@@ -293,17 +529,37 @@ __global__ void __launch_bounds__(kBackWarps * 32)
 
 }  // namespace
 
+namespace {
+
+using ScoredKernel = void (*)(const float*, const float*, int, int, int, ScoreRule, int32_t*, float*,
+                              WsHeader*);
+
+template <int NK>
+ScoredKernel scored_kernel(bool softmax, bool bias) {
+  if (softmax)
+    return bias ? route_scored_kernel<NK, true, true> : route_scored_kernel<NK, true, false>;
+  return bias ? route_scored_kernel<NK, false, true> : route_scored_kernel<NK, false, false>;
+}
+
+}  // namespace
+
 cudaError_t launch_route_scored(const LaunchEnv& env, const float* logits, const float* bias, int T,
                                 int E, int k, const ScoreRule& rule, int32_t* ids, float* gates,
                                 WsHeader* hdr) {
-  const size_t smem = sizeof(double) * kScoredWarps * (size_t)E;
+  const bool softmax = rule.softmax != 0, has_bias = bias != nullptr;
+  const ScoredKernel kernel = E <= 64    ? scored_kernel<2>(softmax, has_bias)
+                              : E <= 128 ? scored_kernel<4>(softmax, has_bias)
+                              : E <= 256 ? scored_kernel<8>(softmax, has_bias)
+                              : E <= 512 ? scored_kernel<16>(softmax, has_bias)
+                                         : scored_kernel<32>(softmax, has_bias);
+  const size_t smem = kScoredWarps * (sizeof(double) * (size_t)E + sizeof(CandArea));
   int per_sm = 1;
-  cudaError_t err = blocks_per_sm((const void*)route_scored_kernel, kScoredWarps * 32, smem, &per_sm);
+  cudaError_t err = blocks_per_sm((const void*)kernel, kScoredWarps * 32, smem, &per_sm);
   if (err != cudaSuccess) return err;
   int64_t grid = ((int64_t)T + kScoredWarps - 1) / kScoredWarps;
   if (grid > (int64_t)per_sm * env.num_sms) grid = (int64_t)per_sm * env.num_sms;
-  return launch_pdl(env, route_scored_kernel, dim3((unsigned)grid), dim3(kScoredWarps * 32), smem,
-                    logits, bias, T, E, k, rule, ids, gates, hdr);
+  return launch_pdl(env, kernel, dim3((unsigned)grid), dim3(kScoredWarps * 32), smem, logits, bias,
+                    T, E, k, rule, ids, gates, hdr);
 }
 
 cudaError_t launch_route_scored_backward(const LaunchEnv& env, const float* logits,
