@@ -20,7 +20,8 @@
 //   2. tau = the k-th largest lane maximum of the kept keys, less the bound: no
 //      key below it can be among the k best; the keys at or above it (k to k+4
 //      of them, usually) are compacted, one a lane;
-//   3. their binary64 keys are ranked against each other, ties by expert.
+//   3. they are ranked by their binary32 keys; where two neighbours among the k
+//      best are closer than the bound, by their binary64 keys, ties by expert.
 // A token whose groups or candidates stay open (ties, masks that leave less
 // than k finite keys, NaN, more than 32 candidates) is decided in binary64
 // throughout, out of line.
@@ -63,7 +64,7 @@ __device__ __forceinline__ int warp_argmax(double v, int id) {
 }
 
 __device__ __forceinline__ double score_d(double l, double m, double inv_sum, bool softmax) {
-  return softmax ? exp(l - m) * inv_sum : 1.0 / (1.0 + exp(-l));
+  return softmax ? exp(l - m) * inv_sum : __drcp_rn(1.0 + exp(-l));
 }
 
 // One token, one warp, everything in binary64.  `key` holds E doubles of this
@@ -160,7 +161,8 @@ __device__ __forceinline__ float scored_gate(double s, int renorm, double scale)
 // while groups are scored), then the candidates.
 constexpr int kCand = 32;
 struct CandArea {
-  double key[kCand], score[kCand];
+  double key[kCand];    // binary64 keys, where they are needed
+  float key32[kCand + 4];
   int expert[kCand];
   int slot[kCand];
 };
@@ -178,8 +180,7 @@ __device__ __forceinline__ float redux_max_f(float v) { return warp_max_nan(v); 
 template <int NK, bool SOFTMAX, bool BIAS>
 __device__ __forceinline__ bool scored_token_fast(const float* __restrict__ row, int E, int k,
                                                   const ScoreRule& R, int lane, uint32_t vmask,
-                                                  const float (&bias)[BIAS ? NK : 1],
-                                                  const float* __restrict__ gbias, float* skey,
+                                                  const float* __restrict__ bias, float* skey,
                                                   CandArea* C, int& sel_e, double& sel_s) {
   float key[NK];
 #pragma unroll
@@ -209,7 +210,7 @@ __device__ __forceinline__ bool scored_token_fast(const float* __restrict__ row,
     if (BIAS) {
       const float inv = __fdividef(1.0f, sum);
 #pragma unroll
-      for (int i = 0; i < NK; ++i) key[i] = ((vmask >> i) & 1u) ? fmaf(key[i], inv, bias[i]) : -INFINITY;
+      for (int i = 0; i < NK; ++i) key[i] = ((vmask >> i) & 1u) ? fmaf(key[i], inv, __ldg(bias + lane + 32 * i)) : -INFINITY;
     } else if (!raw) {  // (unnormalised: the scores' order and that of their sums)
 #pragma unroll
       for (int i = 0; i < NK; ++i) key[i] = ((vmask >> i) & 1u) ? key[i] : -INFINITY;
@@ -218,7 +219,7 @@ __device__ __forceinline__ bool scored_token_fast(const float* __restrict__ row,
 #pragma unroll
     for (int i = 0; i < NK; ++i) {
       const float s = __fdividef(1.0f, 1.0f + __expf(-key[i]));
-      key[i] = ((vmask >> i) & 1u) ? (BIAS ? s + bias[i] : s) : -INFINITY;
+      key[i] = ((vmask >> i) & 1u) ? (BIAS ? s + __ldg(bias + lane + 32 * i) : s) : -INFINITY;
     }
   }
   // How far a key can be from its binary64 value: scores are within 2^-21 of theirs
@@ -228,6 +229,10 @@ __device__ __forceinline__ bool scored_token_fast(const float* __restrict__ row,
   // binary64, whose exponentials could coincide.
   auto bound = [&](float v) { return 1.0e-6f + 2.5e-7f * (fabsf(v) + (raw ? fabsf(m) : 0.0f)); };
 
+#pragma unroll
+  for (int i = 0; i < NK; ++i)
+    if ((vmask >> i) & 1u) skey[lane + 32 * i] = key[i];
+  __syncwarp();
   if (grouped) {
     // Lg lanes a group; they walk its experts in turns that keep the groups' lanes on
     // different banks, and meet in a butterfly of (largest, second largest).
@@ -235,14 +240,11 @@ __device__ __forceinline__ bool scored_token_fast(const float* __restrict__ row,
     const int Lg = 1 << (31 - __clz(32 / R.groups));
     const int g = lane / Lg, sub = lane & (Lg - 1);
     const int steps = (G + Lg - 1) / Lg;
-#pragma unroll
-    for (int i = 0; i < NK; ++i)
-      if ((vmask >> i) & 1u) skey[lane + 32 * i] = key[i];
-    __syncwarp();
     float a = -INFINITY, b = -INFINITY;
     bool odd = false;
     if (g < R.groups) {
       int turn = g < steps ? g : g % steps;
+#pragma unroll 4
       for (int it = 0; it < steps; ++it) {
         const int at = sub + Lg * turn;
         turn = turn + 1 == steps ? 0 : turn + 1;
@@ -316,56 +318,72 @@ __device__ __forceinline__ bool scored_token_fast(const float* __restrict__ row,
     const unsigned any = __ballot_sync(kFull, cm != 0u);
     if (any == 0u) break;
     if (cm != 0u) {
-      C->expert[base + __popc(any & lanemask_lt())] = lane + 32 * (__ffs(cm) - 1);
+      const int e = lane + 32 * (__ffs(cm) - 1), p = base + __popc(any & lanemask_lt());
+      C->expert[p] = e;
+      C->key32[p] = skey[e];
       cm &= cm - 1u;
     }
     base += __popc(any);
   }
+  if (lane < 4) C->key32[total + lane] = -INFINITY;  // pads the last group of four
   __syncwarp();
-  int e = 0;
-  double v = 0.0, s = 0.0;
-  if (lane < total) {
-    e = C->expert[lane];
-    const double l = (double)__ldg(row + e);
-    if (SOFTMAX) {
-      s = exp(l - (double)m);
-      if (BIAS || !R.renorm) s /= (double)sum;
-    } else {
-      s = 1.0 / (1.0 + exp(-l));
-    }
-    v = BIAS ? s + (double)__ldg(gbias + e) : s;
-    C->key[lane] = v;
-  }
-  __syncwarp();
+  // ranked by the binary32 keys (equal ones collide on a slot: a gap of zero below)
+  const int e = lane < total ? C->expert[lane] : 0;
+  const float v = lane < total ? C->key32[lane] : INFINITY;
   int n = 0;
-  if (lane < total)
-    for (int j = 0; j < total; ++j) {
-      const double o = C->key[j];
-      n += (o > v || (o == v && C->expert[j] < e)) ? 1 : 0;
+#pragma unroll 2
+  for (int j = 0; j < total; j += 4) {
+    const float4 q = *reinterpret_cast<const float4*>(C->key32 + j);
+    n += (q.x > v) + (q.y > v) + (q.z > v) + (q.w > v);
+  }
+  float gap = INFINITY;  // to the nearest key below; equal keys: 0
+#pragma unroll 2
+  for (int j = 0; j < total; j += 4) {
+    const float4 q = *reinterpret_cast<const float4*>(C->key32 + j);
+    gap = fminf(gap, q.x < v ? v - q.x : INFINITY);
+    gap = fminf(gap, q.y < v ? v - q.y : INFINITY);
+    gap = fminf(gap, q.z < v ? v - q.z : INFINITY);
+    gap = fminf(gap, q.w < v ? v - q.w : INFINITY);
+  }
+  if (lane < total) C->slot[n] = lane;
+  __syncwarp();
+  const bool near = lane < total && n < k && (!(gap > open) || C->slot[n] != lane);
+  if (__any_sync(kFull, near)) {
+    if (SOFTMAX && BIAS) return false;  // (needs the binary64 sum too)
+    double d = 0.0;
+    if (lane < total) {
+      d = score_d((double)__ldg(row + e), (double)m, 1.0, SOFTMAX);
+      if (BIAS) d += (double)__ldg(bias + e);
+      C->key[lane] = d;
     }
-  __syncwarp();
-  if (lane < total) {
-    C->slot[n] = e;
-    C->score[n] = s;
-    C->key[n] = v;
+    __syncwarp();
+    n = 0;
+    if (lane < total)
+      for (int j = 0; j < total; ++j) {
+        const double o = C->key[j];
+        n += (o > d || (o == d && C->expert[j] < e)) ? 1 : 0;
+      }
+    __syncwarp();
+    if (lane < total) C->slot[n] = lane;
+    __syncwarp();
   }
-  __syncwarp();
-  if (SOFTMAX && BIAS) {
-    // the sum of the exponentials is a binary32 one here: neighbours closer than its
-    // error are left open
-    const bool close = lane < k && lane + 1 < total && !(C->key[lane] - C->key[lane + 1] > (double)open);
-    if (__any_sync(kFull, close)) return false;
+  sel_e = 0;
+  sel_s = 0.0;
+  if (lane < k) {
+    sel_e = C->expert[C->slot[lane]];
+    sel_s = score_d((double)__ldg(row + sel_e), (double)m, 1.0, SOFTMAX);
+    if (SOFTMAX && !R.renorm) sel_s /= (double)sum;
   }
-  sel_e = lane < k ? C->slot[lane] : 0;
-  sel_s = lane < k ? C->score[lane] : 0.0;
   __syncwarp();
   return true;
 }
 
+constexpr int scored_min_blocks(int nk) { return nk <= 8 ? 10 : nk == 16 ? 8 : 6; }
+
 template <int NK, bool SOFTMAX, bool BIAS>
-__global__ void __launch_bounds__(kScoredWarps * 32)
+__global__ void __launch_bounds__(kScoredWarps * 32, scored_min_blocks(NK))
     route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ bias, int T,
-                        int E, int k, ScoreRule R, int32_t* __restrict__ ids,
+                        int E, int k, const __grid_constant__ ScoreRule R, int32_t* __restrict__ ids,
                         float* __restrict__ gates, WsHeader* hdr) {
   extern __shared__ double skey[];
   pdl_wait();
@@ -374,19 +392,17 @@ __global__ void __launch_bounds__(kScoredWarps * 32)
   double* key = skey + (size_t)w * E;
   CandArea* C = reinterpret_cast<CandArea*>(skey + (size_t)kScoredWarps * E) + w;
   uint32_t vmask = 0u;
-  float b[BIAS ? NK : 1];
 #pragma unroll
   for (int i = 0; i < NK; ++i) {
     const int e = lane + 32 * i;
     if (e < E) vmask |= 1u << i;
-    if (BIAS) b[i] = e < E ? __ldg(bias + e) : 0.0f;
   }
   const bool fast = R.groups <= 32 || R.top_groups == R.groups;
   for (int t = blockIdx.x * kScoredWarps + w; t < T; t += gridDim.x * kScoredWarps) {
     const float* row = logits + (size_t)t * E;
     int e = 0;
     double s = 0.0;
-    bool ok = fast && scored_token_fast<NK, SOFTMAX, BIAS>(row, E, k, R, lane, vmask, b, bias,
+    bool ok = fast && scored_token_fast<NK, SOFTMAX, BIAS>(row, E, k, R, lane, vmask, bias,
                                                            reinterpret_cast<float*>(key), C, e, s);
     if (!ok) {
       __syncwarp();
