@@ -157,11 +157,12 @@ __device__ __forceinline__ float scored_gate(double s, int renorm, double scale)
   return (float)(s * scale);
 }
 
-// Per-warp shared memory: E doubles (the exact form's keys; the binary32 keys
-// while groups are scored), then the candidates.
+// Per-warp shared memory: two staged rows of logits (together the exact form's E
+// doubles), the candidates and, where groups are scored from shared memory, the
+// binary32 keys.
 constexpr int kCand = 32;
 struct CandArea {
-  double key[kCand];    // binary64 keys, where they are needed
+  double key[kCand];  // binary64 keys, where they are needed
   float key32[kCand + 4];
   int expert[kCand];
   int slot[kCand];
@@ -173,118 +174,169 @@ __device__ __noinline__ bool scored_token_slow(const float* row, const float* bi
   return scored_token_exact(row, bias, E, k, R, lane, key, sel_e, sel_s);
 }
 
-__device__ __forceinline__ float redux_max_f(float v) { return warp_max_nan(v); }
+// 2^x within 2 units in the last place and 1/x within 1 (flushing subnormals).
+__device__ __forceinline__ float ex2_f(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_f(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.44269504f;
 
-// One token, decided as above; false: not decided.  Lane j < k returns slot j's
-// expert and score.  `skey` holds E floats.
-template <int NK, bool SOFTMAX, bool BIAS>
-__device__ __forceinline__ bool scored_token_fast(const float* __restrict__ row, int E, int k,
-                                                  const ScoreRule& R, int lane, uint32_t vmask,
-                                                  const float* __restrict__ bias, float* skey,
+// How far a binary32 key can be from its binary64 value: a score is within 2^-21
+// (2^x is off by 2^-22, its argument's rounding is damped by the score, the
+// reciprocal and the softmax's sum add 2^-23 each), one addition adds 2^-24 of the
+// key.
+__device__ __forceinline__ float key_bound(float v) { return 1.0e-6f + 2.5e-7f * fabsf(v); }
+
+// What the group scoring needs of the sizes, computed once: unit = 1 << shift lanes a
+// group (a power of two) walk its n pieces (16 bytes, or single keys where groups are
+// not whole pieces) from `start` on, in turns that keep the groups' lanes on different
+// banks.
+struct GroupPlan {
+  int G = 1, shift = 0, n = 1, start = 0;
+  uint32_t magic = 0u;  // e / G == __umulhi(e, magic) for e < 2^16 (G > 1)
+  __device__ void init(int E, int groups, int lane) {
+    G = E / groups;
+    if (groups > 32) return;  // (the exact form's)
+    shift = 31 - __clz(32 / groups);
+    n = (G & 3) == 0 ? G >> 2 : G;
+    const int unit = 1 << shift, g = lane >> shift, sub = lane & (unit - 1);
+    start = sub + unit * g;
+    if (start >= n) start = sub + unit * (g % ((n + unit - 1) >> shift));
+    magic = G > 1 ? (uint32_t)((0x100000000ull + (uint64_t)G - 1) / (uint64_t)G) : 0u;
+  }
+};
+
+// One token, decided as described above; false: not decided.  Lane j < k returns
+// slot j's expert and score.  `row` is the staged row.
+template <int NK, bool SOFTMAX, bool BIAS, bool GROUPED, bool FULL>
+__device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k,
+                                                  const ScoreRule& R, const GroupPlan& L, int lane,
+                                                  uint32_t vmask, const float* __restrict__ bias,
+                                                  float* skey,
                                                   CandArea* C, int& sel_e, double& sel_s) {
+  // without a bias the logits are in the softmax's order (but their sums are not)
+  const bool raw = SOFTMAX && !BIAS && !(GROUPED && R.group_top == 2);
+  auto valid = [&](int i) { return FULL || ((vmask >> i) & 1u) != 0u; };
   float key[NK];
 #pragma unroll
-  for (int i = 0; i < NK; ++i) key[i] = ((vmask >> i) & 1u) ? __ldg(row + lane + 32 * i) : -INFINITY;
-  float m = 0.0f, sum = 1.0f;
-  const bool grouped = R.top_groups < R.groups;
-  // without a bias the logits are in the softmax's order (but their sums are not)
-  const bool raw = SOFTMAX && !BIAS && !(grouped && R.group_top == 2);
+  for (int i = 0; i < NK; ++i) key[i] = valid(i) ? row[lane + 32 * i] : -INFINITY;
+  float m = 0.0f, scale = 1.0f;  // softmax: largest logit, and what 2^.. is multiplied with
   if (SOFTMAX) {
     m = key[0];
 #pragma unroll
     for (int i = 1; i < NK; ++i) m = max2_nan(m, key[i]);
-    m = redux_max_f(m);
-    if (!(fabsf(m) < INFINITY)) return false;  // NaN, or a row without a finite maximum
-    if (!raw || !R.renorm) {
+    if (__any_sync(kFull, m != m)) return false;
+    m = code_float(__reduce_max_sync(kFull, order_code(m)));
+    if (!(fabsf(m) < INFINITY)) return false;  // a row without a finite maximum
+    if (BIAS || !R.renorm) {
       float part = 0.0f;
 #pragma unroll
-      for (int i = 0; i < NK; ++i) {
-        const float p = __expf(key[i] - m);
-        part += p;
-        if (!raw) key[i] = p;
-      }
+      for (int i = 0; i < NK; ++i) part += ex2_f((key[i] - m) * kLog2e);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kFull, part, o);
-      sum = part;
-    }
-    if (BIAS) {
-      const float inv = __fdividef(1.0f, sum);
-#pragma unroll
-      for (int i = 0; i < NK; ++i) key[i] = ((vmask >> i) & 1u) ? fmaf(key[i], inv, __ldg(bias + lane + 32 * i)) : -INFINITY;
-    } else if (!raw) {  // (unnormalised: the scores' order and that of their sums)
-#pragma unroll
-      for (int i = 0; i < NK; ++i) key[i] = ((vmask >> i) & 1u) ? key[i] : -INFINITY;
-    }
-  } else {
-#pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const float s = __fdividef(1.0f, 1.0f + __expf(-key[i]));
-      key[i] = ((vmask >> i) & 1u) ? (BIAS ? s + __ldg(bias + lane + 32 * i) : s) : -INFINITY;
+      scale = __fdividef(1.0f, part);
     }
   }
-  // How far a key can be from its binary64 value: scores are within 2^-21 of theirs
-  // (the fast exponential is off by 2^-22 and its argument's rounding, which the
-  // scores damp; quotient 2^-22; sum of the softmax 2^-22), one addition 2^-24 of the
-  // key.  Logits are exact; two of them closer than 2^-20 of their size are left to
-  // binary64, whose exponentials could coincide.
-  auto bound = [&](float v) { return 1.0e-6f + 2.5e-7f * (fabsf(v) + (raw ? fabsf(m) : 0.0f)); };
-
+  // the key of expert e with logit l
+  auto key_of = [&](float l, int e) -> float {
+    float v;
+    if (SOFTMAX) {
+      if (raw) return l;
+      v = ex2_f((l - m) * kLog2e);
+      return BIAS ? fmaf(v, scale, __ldg(bias + e)) : v;
+    }
+    v = rcp_f(1.0f + ex2_f(l * -kLog2e));
+    return BIAS ? v + __ldg(bias + e) : v;
+  };
+  if (!SOFTMAX || !raw) {
 #pragma unroll
-  for (int i = 0; i < NK; ++i)
-    if ((vmask >> i) & 1u) skey[lane + 32 * i] = key[i];
-  __syncwarp();
-  if (grouped) {
-    // Lg lanes a group; they walk its experts in turns that keep the groups' lanes on
-    // different banks, and meet in a butterfly of (largest, second largest).
-    const int G = E / R.groups;
-    const int Lg = 1 << (31 - __clz(32 / R.groups));
-    const int g = lane / Lg, sub = lane & (Lg - 1);
-    const int steps = (G + Lg - 1) / Lg;
+    for (int i = 0; i < NK; ++i)
+      if (valid(i)) key[i] = key_of(key[i], lane + 32 * i);
+  }
+  // logits are exact; two closer than the bound are left to binary64, whose
+  // exponentials could coincide
+  auto bound = [&](float v) { return key_bound(raw ? fabsf(v) + fabsf(m) : v); };
+
+  if (GROUPED) {
+    const int G = L.G, unit = 1 << L.shift, g = lane >> L.shift, sub = lane & (unit - 1);
+#pragma unroll
+    for (int i = 0; i < NK; ++i)
+      if (valid(i)) skey[lane + 32 * i] = key[i];
+    __syncwarp();
     float a = -INFINITY, b = -INFINITY;
-    bool odd = false;
+    auto take = [&](float v) {
+      b = fmaxf(b, fminf(a, v));
+      a = max2_nan(a, v);
+    };
     if (g < R.groups) {
-      int turn = g < steps ? g : g % steps;
-#pragma unroll 4
-      for (int it = 0; it < steps; ++it) {
-        const int at = sub + Lg * turn;
-        turn = turn + 1 == steps ? 0 : turn + 1;
-        if (at < G) {
-          const float v = skey[g * G + at];
-          odd |= !(v < INFINITY);
-          b = fmaxf(b, fminf(a, v));
-          a = fmaxf(a, v);
+      const float* part = skey + g * G;
+      const int n = L.n;
+      int at = L.start;
+      for (int it = sub; it < n + sub; it += unit) {
+        if (at < n) {
+          if ((G & 3) == 0) {
+            const float4 q = reinterpret_cast<const float4*>(part)[at];
+            take(q.x);
+            take(q.y);
+            take(q.z);
+            take(q.w);
+          } else {
+            take(part[at]);
+          }
         }
+        at += unit;
+        if (at >= n + sub) at = sub;
       }
     }
-    if (__any_sync(kFull, odd)) return false;
-    for (int o = 1; o < Lg; o <<= 1) {
+    if (__any_sync(kFull, !(a < INFINITY))) return false;
+#pragma unroll 1
+    for (int o = 1; o < unit; o <<= 1) {
       const float oa = __shfl_xor_sync(kFull, a, o), ob = __shfl_xor_sync(kFull, b, o);
       b = fmaxf(fminf(a, oa), fmaxf(b, ob));
       a = fmaxf(a, oa);
     }
-    float score = R.group_top == 2 ? a + b : a;
-    if (g >= R.groups || sub != 0) score = -INFINITY;
-    // the largest key among those that scores are made of (a group without a finite
-    // key scores -inf in any precision)
-    const float mag = score == -INFINITY ? 0.0f : fmaxf(fabsf(a), R.group_top == 2 ? fabsf(b) : 0.0f);
-    const float big = redux_max_f(mag);
-    uint32_t kept = 0u;
-    float last = 0.0f;
-    for (int r = 0; r < R.top_groups; ++r) {
-      last = redux_max_f(score);
-      const unsigned hold = __ballot_sync(kFull, score == last);
-      const int who = __ffs(hold) - 1;
-      kept |= 1u << (who / Lg);
-      if (lane == who) score = -INFINITY;
+    float score = -INFINITY, mag = 0.0f;  // lane `unit * g`: group g
+    if (g < R.groups && sub == 0) {
+      score = R.group_top == 2 ? a + b : a;
+      if (score > -INFINITY) mag = fmaxf(fabsf(a), R.group_top == 2 ? fabsf(b) : 0.0f);
     }
-    const float next = redux_max_f(score);
-    if (!(last - next > 4.0f * bound(big))) return false;
-    const uint32_t magic = G > 1 ? (uint32_t)((0x100000000ull + (uint64_t)G - 1) / (uint64_t)G) : 0u;
+    // the kept groups, certain if the best one left out is further off than the errors
+    // of two scores (a group without a finite key scores -inf in any precision)
+    // (maxima on order codes: the integer reduction is one instruction)
+    const float big = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(mag)));
+    uint32_t kept = 0u, scode = order_code(score), best = 0u;
+    for (int r = 0; r < R.top_groups; ++r) {
+      best = __reduce_max_sync(kFull, scode);
+      const int who = __ffs(__ballot_sync(kFull, scode == best)) - 1;
+      kept |= 1u << (who >> L.shift);
+      if (lane == who) scode = 0u;
+    }
+    const uint32_t next = __reduce_max_sync(kFull, scode);
+    // (code 0: no group is left, which does not happen below top_groups = groups)
+    if (!(code_float(best) - code_float(next) > 4.0f * bound(big))) return false;
+    if ((G & 31) == 0) {
+      const int step = G >> 5;
+      int in = 0;
 #pragma unroll
-    for (int i = 0; i < NK; ++i) {
-      const uint32_t e = (uint32_t)(lane + 32 * i);
-      const uint32_t q = G > 1 ? __umulhi(e, magic) : e;
-      if (!((kept >> (q & 31u)) & 1u)) key[i] = -INFINITY;
+      for (int i = 0; i < NK; ++i) {
+        key[i] = (kept & 1u) ? key[i] : -INFINITY;
+        ++in;
+        kept >>= in == step ? 1 : 0;
+        in = in == step ? 0 : in;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < NK; ++i) {
+        const uint32_t e = (uint32_t)(lane + 32 * i);
+        const uint32_t q = G > 1 ? __umulhi(e, L.magic) : e;
+        if (!((kept >> (q & 31u)) & 1u)) key[i] = -INFINITY;
+      }
     }
   }
 
@@ -293,19 +345,19 @@ __device__ __forceinline__ bool scored_token_fast(const float* __restrict__ row,
 #pragma unroll
   for (int i = 1; i + 1 < NK; i += 2) mm = max3_nan(mm, key[i], key[i + 1]);
   mm = max2_nan(mm, key[NK - 1]);
-  const float wmax = redux_max_f(mm);
-  if (!(wmax < INFINITY)) return false;
+  if (__any_sync(kFull, !(mm < INFINITY))) return false;
   uint32_t code = (order_code(mm) & ~31u) | (uint32_t)(31 - lane);
-  uint32_t top = 0u;
-#pragma unroll 1
-  for (int j = 0; j < k; ++j) {
-    top = __reduce_max_sync(kFull, code);
+  uint32_t top = __reduce_max_sync(kFull, code);
+  const float wmax = code_float(top | 31u);  // no lane's maximum is larger
+#pragma unroll 2
+  for (int j = 1; j < k; ++j) {
     code = code == top ? 0u : code;
+    top = __reduce_max_sync(kFull, code);
   }
   if (top < 0x00800000u) return false;  // a lane without a finite key among the k
   const float tau = code_float(top & ~31u);
-  if (raw && !(tau - m > -700.0f)) return false;  // scores that vanish in binary64 tie
-  const float open = 2.0f * bound(fmaxf(fabsf(tau), BIAS ? fabsf(wmax) : 0.0f));
+  if (SOFTMAX && raw && !(tau - m > -700.0f)) return false;  // scores that vanish in binary64 tie
+  const float open = 2.0f * bound(fmaxf(fabsf(tau), fabsf(wmax)));
   const float thr = tau - open;
   uint32_t cm = 0u;
 #pragma unroll
@@ -318,41 +370,33 @@ __device__ __forceinline__ bool scored_token_fast(const float* __restrict__ row,
     const unsigned any = __ballot_sync(kFull, cm != 0u);
     if (any == 0u) break;
     if (cm != 0u) {
-      const int e = lane + 32 * (__ffs(cm) - 1), p = base + __popc(any & lanemask_lt());
-      C->expert[p] = e;
-      C->key32[p] = skey[e];
+      C->expert[base + __popc(any & lanemask_lt())] = lane + 32 * (__ffs(cm) - 1);
       cm &= cm - 1u;
     }
     base += __popc(any);
   }
-  if (lane < 4) C->key32[total + lane] = -INFINITY;  // pads the last group of four
   __syncwarp();
-  // ranked by the binary32 keys (equal ones collide on a slot: a gap of zero below)
   const int e = lane < total ? C->expert[lane] : 0;
-  const float v = lane < total ? C->key32[lane] : INFINITY;
-  int n = 0;
+  const float v = lane < total ? key_of(row[e], e) : -INFINITY;
+  C->key32[lane] = v;
+  if (lane < 4) C->key32[kCand + lane] = -INFINITY;
+  __syncwarp();
+  // ranked by the binary32 keys: larger ones, and whether one is no further below than
+  // the bound (equal ones, the key itself among them, do not count twice)
+  int n = 0, within = 0;
+  const float low = v - open;
 #pragma unroll 2
   for (int j = 0; j < total; j += 4) {
     const float4 q = *reinterpret_cast<const float4*>(C->key32 + j);
     n += (q.x > v) + (q.y > v) + (q.z > v) + (q.w > v);
-  }
-  float gap = INFINITY;  // to the nearest key below; equal keys: 0
-#pragma unroll 2
-  for (int j = 0; j < total; j += 4) {
-    const float4 q = *reinterpret_cast<const float4*>(C->key32 + j);
-    gap = fminf(gap, q.x < v ? v - q.x : INFINITY);
-    gap = fminf(gap, q.y < v ? v - q.y : INFINITY);
-    gap = fminf(gap, q.z < v ? v - q.z : INFINITY);
-    gap = fminf(gap, q.w < v ? v - q.w : INFINITY);
+    within += (q.x >= low) + (q.y >= low) + (q.z >= low) + (q.w >= low);
   }
   if (lane < total) C->slot[n] = lane;
-  __syncwarp();
-  const bool near = lane < total && n < k && (!(gap > open) || C->slot[n] != lane);
-  if (__any_sync(kFull, near)) {
+  if (__any_sync(kFull, lane < total && n < k && within - n != 1)) {
     if (SOFTMAX && BIAS) return false;  // (needs the binary64 sum too)
     double d = 0.0;
     if (lane < total) {
-      d = score_d((double)__ldg(row + e), (double)m, 1.0, SOFTMAX);
+      d = score_d((double)row[e], (double)m, 1.0, SOFTMAX);
       if (BIAS) d += (double)__ldg(bias + e);
       C->key[lane] = d;
     }
@@ -363,50 +407,92 @@ __device__ __forceinline__ bool scored_token_fast(const float* __restrict__ row,
         const double o = C->key[j];
         n += (o > d || (o == d && C->expert[j] < e)) ? 1 : 0;
       }
-    __syncwarp();
     if (lane < total) C->slot[n] = lane;
-    __syncwarp();
   }
+  __syncwarp();
   sel_e = 0;
   sel_s = 0.0;
   if (lane < k) {
     sel_e = C->expert[C->slot[lane]];
-    sel_s = score_d((double)__ldg(row + sel_e), (double)m, 1.0, SOFTMAX);
-    if (SOFTMAX && !R.renorm) sel_s /= (double)sum;
+    sel_s = score_d((double)row[sel_e], (double)m, 1.0, SOFTMAX);
+    if (SOFTMAX && !R.renorm) sel_s *= (double)scale;
   }
   __syncwarp();
   return true;
 }
 
-constexpr int scored_min_blocks(int nk) { return nk <= 8 ? 10 : nk == 16 ? 8 : 6; }
+// Stage a row: this lane's 16-byte pieces, or words where rows are not aligned.
+__device__ __forceinline__ void stage_row(float* dst, const float* __restrict__ src, int E, int lane,
+                                          bool vec) {
+  if (vec) {
+    for (int i = lane * 4; i < E; i += 128)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(
+                       static_cast<uint32_t>(__cvta_generic_to_shared(dst + i))),
+                   "l"(src + i)
+                   : "memory");
+  } else {
+    for (int i = lane; i < E; i += 32)
+      asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(
+                       static_cast<uint32_t>(__cvta_generic_to_shared(dst + i))),
+                   "l"(src + i)
+                   : "memory");
+  }
+  asm volatile("cp.async.commit_group;" ::: "memory");
+}
 
-template <int NK, bool SOFTMAX, bool BIAS>
+// Floats of a staged row, and bytes of a warp's shared memory.
+__host__ __device__ constexpr int row_floats(int E) { return (E + 3) / 4 * 4; }
+__host__ __device__ constexpr size_t warp_bytes(int E, bool keys) {
+  return sizeof(float) * (size_t)row_floats(E) * (keys ? 3 : 2) + sizeof(CandArea);
+}
+
+constexpr int scored_min_blocks(int nk) { return nk <= 8 ? 8 : nk == 16 ? 7 : 4; }
+
+template <int NK, bool SOFTMAX, bool BIAS, bool GROUPED, bool FULL>
 __global__ void __launch_bounds__(kScoredWarps * 32, scored_min_blocks(NK))
     route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ bias, int T,
-                        int E, int k, const __grid_constant__ ScoreRule R, int32_t* __restrict__ ids,
-                        float* __restrict__ gates, WsHeader* hdr) {
-  extern __shared__ double skey[];
+                        int E, int k, const __grid_constant__ ScoreRule R, int vec,
+                        int32_t* __restrict__ ids, float* __restrict__ gates, WsHeader* hdr) {
+  extern __shared__ __align__(16) uint8_t smem[];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  double* key = skey + (size_t)w * E;
-  CandArea* C = reinterpret_cast<CandArea*>(skey + (size_t)kScoredWarps * E) + w;
+  uint8_t* mine = smem + (size_t)w * warp_bytes(E, GROUPED);
+  CandArea* C = reinterpret_cast<CandArea*>(mine);
+  float* rows = reinterpret_cast<float*>(mine + sizeof(CandArea));
+  const int stride = row_floats(E);
+  float* skey = rows + 2 * stride;
   uint32_t vmask = 0u;
 #pragma unroll
-  for (int i = 0; i < NK; ++i) {
-    const int e = lane + 32 * i;
-    if (e < E) vmask |= 1u << i;
-  }
-  const bool fast = R.groups <= 32 || R.top_groups == R.groups;
-  for (int t = blockIdx.x * kScoredWarps + w; t < T; t += gridDim.x * kScoredWarps) {
-    const float* row = logits + (size_t)t * E;
+  for (int i = 0; i < NK; ++i)
+    if (lane + 32 * i < E) vmask |= 1u << i;
+  const bool fast = !GROUPED || R.groups <= 32;
+  GroupPlan plan;
+  if (GROUPED) plan.init(E, R.groups, lane);
+  const int step = gridDim.x * kScoredWarps;
+  int t = blockIdx.x * kScoredWarps + w, turn = 0;
+  if (t < T) stage_row(rows, logits + (size_t)t * E, E, lane, vec != 0);
+  for (; t < T; t += step, turn ^= 1) {
+    if (t + step < T) {
+      stage_row(rows + (turn ^ 1) * stride, logits + (size_t)(t + step) * E, E, lane, vec != 0);
+      asm volatile("cp.async.wait_group 1;" ::: "memory");
+    } else {
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    __syncwarp();
     int e = 0;
     double s = 0.0;
-    bool ok = fast && scored_token_fast<NK, SOFTMAX, BIAS>(row, E, k, R, lane, vmask, bias,
-                                                           reinterpret_cast<float*>(key), C, e, s);
+    bool ok = fast && scored_token_fast<NK, SOFTMAX, BIAS, GROUPED, FULL>(rows + turn * stride, E, k, R, plan, lane,
+                                                                vmask, bias, skey, C, e, s);
     if (!ok) {
+      // the exact form's keys take both staged rows: the next one is staged again
+      asm volatile("cp.async.wait_group 0;" ::: "memory");
       __syncwarp();
-      ok = scored_token_slow(row, bias, E, k, R, lane, key, e, s);
+      ok = scored_token_slow(logits + (size_t)t * E, bias, E, k, R, lane,
+                             reinterpret_cast<double*>(rows), e, s);
+      __syncwarp();
+      if (t + step < T)
+        stage_row(rows + (turn ^ 1) * stride, logits + (size_t)(t + step) * E, E, lane, vec != 0);
     }
     float g = 0.0f;
     if (ok) {
@@ -547,14 +633,21 @@ __global__ void __launch_bounds__(kBackWarps * 32)
 
 namespace {
 
-using ScoredKernel = void (*)(const float*, const float*, int, int, int, ScoreRule, int32_t*, float*,
-                              WsHeader*);
+using ScoredKernel = void (*)(const float*, const float*, int, int, int, ScoreRule, int, int32_t*,
+                              float*, WsHeader*);
 
-template <int NK>
-ScoredKernel scored_kernel(bool softmax, bool bias) {
-  if (softmax)
-    return bias ? route_scored_kernel<NK, true, true> : route_scored_kernel<NK, true, false>;
-  return bias ? route_scored_kernel<NK, false, true> : route_scored_kernel<NK, false, false>;
+template <int NK, bool SOFTMAX, bool BIAS, bool GROUPED>
+ScoredKernel scored_kernel(int E) {
+  return E == 32 * NK ? route_scored_kernel<NK, SOFTMAX, BIAS, GROUPED, true>
+                      : route_scored_kernel<NK, SOFTMAX, BIAS, GROUPED, false>;
+}
+template <bool SOFTMAX, bool BIAS, bool GROUPED>
+ScoredKernel scored_kernel(int E) {
+  return E <= 64    ? scored_kernel<2, SOFTMAX, BIAS, GROUPED>(E)
+         : E <= 128 ? scored_kernel<4, SOFTMAX, BIAS, GROUPED>(E)
+         : E <= 256 ? scored_kernel<8, SOFTMAX, BIAS, GROUPED>(E)
+         : E <= 512 ? scored_kernel<16, SOFTMAX, BIAS, GROUPED>(E)
+                    : scored_kernel<32, SOFTMAX, BIAS, GROUPED>(E);
 }
 
 }  // namespace
@@ -562,20 +655,28 @@ ScoredKernel scored_kernel(bool softmax, bool bias) {
 cudaError_t launch_route_scored(const LaunchEnv& env, const float* logits, const float* bias, int T,
                                 int E, int k, const ScoreRule& rule, int32_t* ids, float* gates,
                                 WsHeader* hdr) {
-  const bool softmax = rule.softmax != 0, has_bias = bias != nullptr;
-  const ScoredKernel kernel = E <= 64    ? scored_kernel<2>(softmax, has_bias)
-                              : E <= 128 ? scored_kernel<4>(softmax, has_bias)
-                              : E <= 256 ? scored_kernel<8>(softmax, has_bias)
-                              : E <= 512 ? scored_kernel<16>(softmax, has_bias)
-                                         : scored_kernel<32>(softmax, has_bias);
-  const size_t smem = kScoredWarps * (sizeof(double) * (size_t)E + sizeof(CandArea));
+  const bool grouped = rule.top_groups < rule.groups;
+  const int form = (rule.softmax ? 4 : 0) + (bias != nullptr ? 2 : 0) + (grouped ? 1 : 0);
+  ScoredKernel kernel = nullptr;
+  switch (form) {
+    case 0: kernel = scored_kernel<false, false, false>(E); break;
+    case 1: kernel = scored_kernel<false, false, true>(E); break;
+    case 2: kernel = scored_kernel<false, true, false>(E); break;
+    case 3: kernel = scored_kernel<false, true, true>(E); break;
+    case 4: kernel = scored_kernel<true, false, false>(E); break;
+    case 5: kernel = scored_kernel<true, false, true>(E); break;
+    case 6: kernel = scored_kernel<true, true, false>(E); break;
+    default: kernel = scored_kernel<true, true, true>(E); break;
+  }
+  const int vec = (E % 4) == 0 && (reinterpret_cast<uintptr_t>(logits) % 16) == 0;
+  const size_t smem = kScoredWarps * warp_bytes(E, grouped);
   int per_sm = 1;
   cudaError_t err = blocks_per_sm((const void*)kernel, kScoredWarps * 32, smem, &per_sm);
   if (err != cudaSuccess) return err;
   int64_t grid = ((int64_t)T + kScoredWarps - 1) / kScoredWarps;
   if (grid > (int64_t)per_sm * env.num_sms) grid = (int64_t)per_sm * env.num_sms;
   return launch_pdl(env, kernel, dim3((unsigned)grid), dim3(kScoredWarps * 32), smem, logits, bias,
-                    T, E, k, rule, ids, gates, hdr);
+                    T, E, k, rule, vec, ids, gates, hdr);
 }
 
 cudaError_t launch_route_scored_backward(const LaunchEnv& env, const float* logits,
