@@ -45,7 +45,7 @@ constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = (4 + kEpiWarps) * 32;
 // Staging: two 32 x 32 bf16 blocks a warp; weights gradient one of 32 x 128.
 constexpr int epi_bytes(bool weights) { return kEpiWarps * (weights ? 8192 : 4096); }
-constexpr int kMaxSlice = kABytes + 2 * 128 * kBK * 2;
+constexpr int kMaxSlice = kABytes + 128 * kBK * 2;
 constexpr int kTmemCols = 512;
 constexpr uint64_t kWaitNs = 2000000000ull;
 
@@ -70,7 +70,7 @@ struct GemmParams {
   int kdim;    // contraction length (weights gradient: per expert)
   int cols;    // weights gradient: columns of x
   int band;    // token tiles an expert walks together
-  int max_n;   // columns of a tile, at most (256 or 512)
+  int adapt;   // choose the tiles' height by the rounds they take
   int ring;    // bytes of the operand ring
   int sorted;  // experts in descending order of their rows (see my_tile)
   int act;
@@ -123,11 +123,20 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
   return r;
 }
 
-// A tile: its expert, channel tile, first row (weights gradient: column) and
-// rows; one or two accumulators ("parts") of `n` columns each.
+// A tile: its expert, channel tile, first row (weights gradient: column) and rows;
+// n columns of D.  (Tiles of up to 512 tokens over two accumulators read the
+// weights once instead of twice, but leave nothing for the epilogue to overlap with:
+// Prefill's first product was as fast, a dense product of 16384 rows a third slower.)
 struct Tile {
-  int e, seg, c, row0, rows, parts, n;  // seg: the expert's place in the segment table
+  int e, seg, c, row0, rows, n;  // seg: the expert's place in the segment table
 };
+
+// Tile heights to choose from: 256 - 32 c.
+constexpr int kHeights = 8;
+// Time of a 64-deep slice of a tile of n rows, in cycles: the matrix instructions'
+// 2 n, or what bringing its operands costs (measured: 335 ns for the narrowest, 450
+// for 256 rows with weights from HBM).
+__device__ __forceinline__ int slice_cost(int n) { return max(2 * n, 230 + (4 * n) / 5); }
 
 // Token rows that copies bring for `half` (a multiple of 16, up to 128) wanted:
 // one box of 32, 64 or 128, or 64 + 32.  Few large copies: with boxes of 32
@@ -169,6 +178,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   __shared__ uint32_t tmem_slot;
   __shared__ int abort_flag;
   __shared__ unsigned long long rows_sum;
+  __shared__ int tiles_at[kHeights];
   __shared__ int32_t warp_tot[kGemmThreads / 32];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
@@ -198,6 +208,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     mbar_init(&drain, 1);
     abort_flag = 0;
     rows_sum = 0ull;
+    for (int c = 0; c < kHeights; ++c) tiles_at[c] = 0;
     mbar_fence_init();
     tma_prefetch_map(&P.ma);
     tma_prefetch_map(&P.mb[0]);
@@ -219,6 +230,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     }
   }
   if (my_rows != 0ull) atomicAdd(&rows_sum, my_rows);
+  const int ctiles = (P.M + kTileM - 1) / kTileM;
+  int height = kBN;
+  if (MODE != kWeights && P.adapt) {
+    // Few rounds of tiles: the height whose rounds take least (one round more than
+    // needed costs a dense product of 16387 rows an eighth).
+#pragma unroll
+    for (int c = 0; c < kHeights; ++c) {
+      int n = 0;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i)
+        if (tid + i * kGemmThreads < P.E) n += (seg[i].rows + kBN - 32 * c - 1) / (kBN - 32 * c);
+      n = (int)__reduce_add_sync(kFull, (unsigned)n);
+      if (lane == 0 && n > 0) atomicAdd(&tiles_at[c], n);
+    }
+    __syncthreads();
+    int64_t best = INT64_MAX;
+    for (int c = 0; c < kHeights; ++c) {
+      const int64_t rounds = ((int64_t)tiles_at[c] * ctiles + pairs - 1) / pairs;
+      const int64_t cost = rounds * slice_cost(kBN - 32 * c);
+      if (cost < best) {
+        best = cost;
+        height = kBN - 32 * c;
+      }
+    }
+  }
   int at[kMine];
 #pragma unroll
   for (int i = 0; i < kMine; ++i) at[i] = tid + i * kGemmThreads;
@@ -245,7 +281,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       seg_off[at[i]] = seg[i].off;
       seg_rows[at[i]] = seg[i].rows;
       if (MODE != kWeights) {
-        first[at[i]] = (seg[i].rows + P.max_n - 1) / P.max_n;
+        first[at[i]] = (seg[i].rows + height - 1) / height;
         expert[at[i]] = e;
       }
     }
@@ -255,7 +291,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   cluster_sync_all();  // the other CTA's barriers are ready too
   tc_fence_after();
   const uint32_t tmem = tmem_slot;
-  const int ctiles = (P.M + kTileM - 1) / kTileM;
   int total;
   if constexpr (MODE == kWeights) {
     total = P.E * ctiles * ((P.cols + kBN - 1) / kBN);
@@ -292,7 +327,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       r.c = u / nt;
       r.row0 = (u - r.c * nt) * kBN;  // first column
       r.rows = min(kBN, P.cols - r.row0);
-      r.parts = 1;
       r.n = (r.rows + 31) & ~31;
     } else {
       const int u = t / ctiles;
@@ -317,8 +351,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       r.c = v / nb;
       r.row0 = n * per;
       r.rows = min(per, seg_rows[lo] - r.row0);
-      r.parts = r.rows > kBN ? 2 : 1;
-      r.n = r.parts == 2 ? ((r.rows + 1) / 2 + 31) & ~31 : (r.rows + 31) & ~31;
+      r.n = (r.rows + 31) & ~31;
     }
     return r;
   };
@@ -344,7 +377,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   // there, at the ring's start.  Every role places the slices alike.
   auto slice_bytes = [&](const Tile& r) -> int {
     return kABytes + (MODE == kWeights ? ((r.n / 2 + 63) >> 6) * 8192
-                                       : r.parts * box_rows(r.n / 2) * (kBK * 2));
+                                       : box_rows(r.n / 2) * (kBK * 2));
   };
   auto place = [&](int& head, int bytes) -> int {
     if (head + bytes > P.ring) head = 0;
@@ -438,16 +471,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
               tma_load_2d(b, &P.mb[0], col, row + k0, bar);
               if (half > 64) tma_load_2d(b + 8192, &P.mb[0], col + 64, row + k0, bar);
             } else {
-              int y = row;
-              for (int p = 0; p < r.parts; ++p, y += r.n, b += fetched * (kBK * 2)) {
-                if (fetched == 128) {
-                  tma_load_2d(b, &P.mb[2], k0, y, bar);
-                } else if (fetched == 32) {
-                  tma_load_2d(b, &P.mb[0], k0, y, bar);
-                } else {
-                  tma_load_2d(b, &P.mb[1], k0, y, bar);
-                  if (fetched == 96) tma_load_2d(b + 8192, &P.mb[0], k0, y + 64, bar);
-                }
+              if (fetched == 128) {
+                tma_load_2d(b, &P.mb[2], k0, row, bar);
+              } else if (fetched == 32) {
+                tma_load_2d(b, &P.mb[0], k0, row, bar);
+              } else {
+                tma_load_2d(b, &P.mb[1], k0, row, bar);
+                if (fetched == 96) tma_load_2d(b + 8192, &P.mb[0], k0, row + 64, bar);
               }
             }
           }
@@ -479,14 +509,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         const Tile r = tile_of(t);
         const int depth = MODE == kWeights ? seg_rows[r.seg] : P.kdim;
         if (depth == 0) continue;
-        for (int p = 0; p < r.parts && ok; ++p)
-          ok = wait(&tempty[(nacc + p) & 1u], (((nacc + p) >> 1) & 1u) ^ 1u);
+        ok = wait(&tempty[nacc & 1u], ((nacc >> 1) & 1u) ^ 1u);
         if (!ok) break;
         tc_fence_after();
         const uint32_t idesc = umma_idesc(2 * kBM, (uint32_t)r.n, a_mn, b_mn);
         const int bytes = slice_bytes(r);
-        const uint64_t part = (uint64_t)(r.parts == 2 ? (bytes - kABytes) / 32 : 0);
-        const uint32_t d0 = tmem + (nacc & 1u) * 256u, d1 = tmem + (~nacc & 1u) * 256u;
+        const uint32_t d = tmem + (nacc & 1u) * 256u;
         for (int k0 = 0; k0 < depth; k0 += kBK, ++it) {
           const uint32_t s = it % kSlots;
           const int at = place(head, bytes);
@@ -506,16 +534,12 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
           for (int q = 0; q < kBK / 16; ++q)
             if (MODE != kWeights || q < ksteps)
-              umma_f16(d0, da + q * sa16, db + q * sb16, idesc, k0 > 0 || q > 0);
-          if (MODE != kWeights && r.parts == 2) {
-#pragma unroll
-            for (int q = 0; q < kBK / 16; ++q)
-              umma_f16(d1, da + q * sa16, db + part + q * sb16, idesc, k0 > 0 || q > 0);
-          }
+              umma_f16(d, da + q * sa16, db + q * sb16, idesc, k0 > 0 || q > 0);
           umma_commit(&empty[s]);
         }
         if (!ok) break;
-        for (int p = 0; p < r.parts; ++p, ++nacc) umma_commit(&tfull[nacc & 1u]);
+        umma_commit(&tfull[nacc & 1u]);
+        ++nacc;
       }
       if (!ok) {  // what was issued ends before the pair does
         umma_commit(&drain);
@@ -620,205 +644,202 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const int ch0 = GATED ? r.c * kTileM + (int)rank * 64 + (q & 1) * 32
                             : r.c * kTileM + (int)rank * kBM + q * 32;
       const int nc = P.M - ch0;
-      for (int p = 0; p < r.parts && ok; ++p) {
-        const uint32_t acc = nacc & 1u;
-        if (!empty_sum) {
-          if (!warp_wait(&tfull[acc], (nacc >> 1) & 1u)) {
-            ok = false;
-            break;
-          }
-          tc_fence_after();
-          ++nacc;
+      const uint32_t acc = nacc & 1u;
+      if (!empty_sum) {
+        if (!warp_wait(&tfull[acc], (nacc >> 1) & 1u)) {
+          ok = false;
+          break;
         }
-        const uint32_t d = tmem + acc * 256u + ((uint32_t)(q * 32) << 16);
-        const int row0 = r.row0 + p * r.n;
-        const int rows = min(r.n, r.row0 + r.rows - row0);
-        const int nchunks = (rows + 31) >> 5;
-        if constexpr (MODE == kWeights) {
-          // Warps 4..7 take columns 0..127, warps 8..11 the others, 64 at a time.  A lane
-          // holds 32 columns of one row of dW; 32 rows of 128 bytes (16-byte pieces
-          // swizzled by the row) are staged in one of two 4 KiB blocks and stored as one
-          // box while the other block is filled.  (Boxes of 32 x 32 held the gradient of
-          // 256-row experts at 3.2 TB/s, one block of 8 KiB at 3.7.)
-          const int col0 = half * 128, ncols = min(128, rows - col0);
-          uint32_t v[32];
+        tc_fence_after();
+        ++nacc;
+      }
+      const uint32_t d = tmem + acc * 256u + ((uint32_t)(q * 32) << 16);
+      const int row0 = r.row0, rows = r.rows;
+      const int nchunks = (rows + 31) >> 5;
+      if constexpr (MODE == kWeights) {
+        // Warps 4..7 take columns 0..127, warps 8..11 the others, 64 at a time.  A lane
+        // holds 32 columns of one row of dW; 32 rows of 128 bytes (16-byte pieces
+        // swizzled by the row) are staged in one of two 4 KiB blocks and stored as one
+        // box while the other block is filled.  (Boxes of 32 x 32 held the gradient of
+        // 256-row experts at 3.2 TB/s, one block of 8 KiB at 3.7.)
+        const int col0 = half * 128, ncols = min(128, rows - col0);
+        uint32_t v[32];
 #pragma unroll
-          for (int i = 0; i < 32; ++i) v[i] = 0u;
-          if (!empty_sum && ncols > 0) tmem_ld32(d + col0, v);
+        for (int i = 0; i < 32; ++i) v[i] = 0u;
+        if (!empty_sum && ncols > 0) tmem_ld32(d + col0, v);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            if (j * 32 < ncols) {
-              uint8_t* buf = epi + (wid - 4) * 8192 + (j >> 1) * 4096;
-              if ((j & 1) == 0) {
-                if (elect_one()) bulk_wait_read<1>();
-                __syncwarp();
-              }
-              uint32_t w[16];
-              if (!empty_sum) tmem_ld_wait(v);
-#pragma unroll
-              for (int i = 0; i < 16; ++i)
-                w[i] = pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
-              if (!empty_sum && (j + 1) * 32 < ncols) tmem_ld32(d + col0 + (j + 1) * 32, v);
-#pragma unroll
-              for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<uint4*>(buf + lane * 128 + ((((j & 1) * 4 + i) ^ (lane & 7)) << 4)) =
-                    make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-              if ((j & 1) != 0 || (j + 1) * 32 >= ncols) {
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (elect_one()) {
-                  if (nc > 0) tma_store_3d(&P.mo, buf, row0 + col0 + (j >> 1) * 64, ch0, r.e);
-                  bulk_commit();
-                }
-              }
+        for (int j = 0; j < 4; ++j) {
+          if (j * 32 < ncols) {
+            uint8_t* buf = epi + (wid - 4) * 8192 + (j >> 1) * 4096;
+            if ((j & 1) == 0) {
+              if (elect_one()) bulk_wait_read<1>();
+              __syncwarp();
             }
-          }
-          // (both blocks take turns: a tile that ends after the first gives the second's turn)
-          if (ncols <= 64 && elect_one()) bulk_commit();
-        } else {
-          const int64_t row = (int64_t)seg_off[r.seg] + row0;
-          const bool up_half = GATED && q >= 2;
-          // this thread's channels: ch0 + lane/4 + 8c
-          float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-          if (MODE == kFwd && P.bias != nullptr) {
-            const float* bp = P.bias + (size_t)r.e * P.M * (GATED ? 2 : 1) + (up_half ? P.M : 0) + ch0;
+            uint32_t w[16];
+            if (!empty_sum) tmem_ld_wait(v);
 #pragma unroll
-            for (int c = 0; c < 4; ++c) {
-              const int ch = (lane >> 2) + 8 * c;
-              if (ch < nc) bias[c] = __ldg(bp + ch);
-            }
-          }
-          uint32_t next[32];
-          if (half < nchunks) load_block(d + half * 32, next);
-          for (int j = half; j < nchunks; j += 2) {
-            const int64_t row_j = row + j * 32;
-            const int nr = rows - j * 32;
-            // tokens whose results this warp writes: all 32, or gated its half
-            const int tok0 = up_half ? 16 : 0;
-            constexpr int kTok = GATED ? 16 : 32;
-            // the residual's block, on its way while the accumulator is read
-            uint4 res[MODE == kFwd ? kTok / 8 : 1];
-            if constexpr (MODE == kFwd) {
-              if (P.residual != nullptr) {
-                const uint16_t* src = P.residual + (row_j + tok0) * P.M + ch0;
+            for (int i = 0; i < 16; ++i)
+              w[i] = pack2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
+            if (!empty_sum && (j + 1) * 32 < ncols) tmem_ld32(d + col0 + (j + 1) * 32, v);
 #pragma unroll
-                for (int i = 0; i < kTok / 8; ++i) {
-                  const int rr = i * 8 + frow;
-                  res[i] = rr + tok0 < nr && fcol < nc
-                               ? *reinterpret_cast<const uint4*>(src + (size_t)rr * P.M + fcol)
-                               : make_uint4(0, 0, 0, 0);
-                }
-              }
-            }
-            tmem_ld_wait(next);
-            float z[32];
-#pragma unroll
-            for (int i = 0; i < 32; ++i)
-              z[i] = __uint_as_float(next[i]) + bias[(i >> 4) * 2 + ((i >> 1) & 1)];
-            if (j + 2 < nchunks) load_block(d + (j + 2) * 32, next);
-            if constexpr (MODE == kFwd) {
-              if (P.pre != nullptr) {
-                const int wide = P.M * (GATED ? 2 : 1);
-                uint8_t* buf = open_block();
-#pragma unroll
-                for (int i = 0; i < 4; ++i) stage8(buf, i, z, i, 4);
-                // (a gate half's block may reach into the up half's columns: lane stores)
-                const bool inside = !GATED || up_half || nc >= 32;
-                close_tokens(buf, &P.mp, P.pre, row_j, (up_half ? P.M : 0) + ch0, wide,
-                             inside ? 32 : INT_MAX, nr, nc);
-              }
-            }
-            float y[kTok];  // the results: fragments of kTok / 8 token groups
-            if constexpr (GATED) {
-              // lanes 0..63 of the accumulator are gates, 64..127 the same channels' ups.
-              // The gate's warp takes tokens 0..15, the up's 16..31: each hands the other
-              // its 16 values a thread through a staging block, in fp32.
-              uint64_t* bar = &swap[half * 2 + (q & 1)];
-              uint8_t* buf = open_block();
-              float4* mine = reinterpret_cast<float4*>(buf) + lane;
-              const float4* theirs =
-                  reinterpret_cast<const float4*>(epi + ((wid - 4) ^ 2) * 4096 + (buf - blocks)) + lane;
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {  // (h, j) = (i / 2, i % 2 of the pair handed over)
-                const int lo = (i >> 1) * 16 + (i & 1) * 4, hi = lo + 8;
-                mine[i * 32] = up_half ? make_float4(z[lo], z[lo + 1], z[lo + 2], z[lo + 3])
-                                       : make_float4(z[hi], z[hi + 1], z[hi + 2], z[hi + 3]);
-              }
+            for (int i = 0; i < 4; ++i)
+              *reinterpret_cast<uint4*>(buf + lane * 128 + ((((j & 1) * 4 + i) ^ (lane & 7)) << 4)) =
+                  make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            if ((j & 1) != 0 || (j + 1) * 32 >= ncols) {
+              fence_proxy_async_smem();
               __syncwarp();
               if (elect_one()) {
+                if (nc > 0) tma_store_3d(&P.mo, buf, row0 + col0 + (j >> 1) * 64, ch0, r.e);
                 bulk_commit();
-                mbar_arrive(bar);
-              }
-              if (!warp_wait(bar, nswap++ & 1u)) {
-                ok = false;
-                break;
-              }
-              float4 other[4];
-#pragma unroll
-              for (int i = 0; i < 4; ++i) other[i] = theirs[i * 32];
-              __syncwarp();
-              if (lane == 0) mbar_arrive(bar);
-              if (!warp_wait(bar, nswap++ & 1u)) {
-                ok = false;
-                break;
-              }
-#pragma unroll
-              for (int i = 0; i < 4; ++i) {
-                const int lo = (i >> 1) * 16 + (i & 1) * 4, hi = lo + 8;
-                const float o[4] = {other[i].x, other[i].y, other[i].z, other[i].w};
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                  const float g = up_half ? o[u] : z[lo + u], v = up_half ? z[hi + u] : o[u];
-                  y[i * 4 + u] = g * sigmoid_f(g) * v;
-                }
-              }
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) y[i] = z[i];
-              if (MODE == kFwd) {
-                if (P.act == MOE_ACT_RELU) {
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) y[i] = z[i] < 0.0f ? 0.0f : z[i];
-                } else if (P.act == MOE_ACT_GELU) {
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) y[i] = gelu_f(z[i]);
-                } else if (P.act == MOE_ACT_SILU) {
-#pragma unroll
-                  for (int i = 0; i < 32; ++i) y[i] = z[i] * sigmoid_f(z[i]);
-                }
               }
             }
-            uint8_t* buf = open_block();
-            if constexpr (MODE == kFwd) {
-              if (P.residual != nullptr) {
-                // through the staging block into the fragments; added in fp32
-#pragma unroll
-                for (int i = 0; i < kTok / 8; ++i) *piece(buf, i * 8 + frow) = res[i];
-                __syncwarp();
-#pragma unroll
-                for (int i = 0; i < kTok / 8; ++i) {
-                  uint32_t f[4];
-                  ldmatrix_t(smem_addr(buf) + t_addr + i * 512, f);
-#pragma unroll
-                  for (int c = 0; c < 4; ++c) {
-                    float* at = y + (c >> 1) * (kTok / 2) + 4 * i + (c & 1) * 2;
-                    at[0] += bf16lo(f[c]);
-                    at[1] += bf16hi(f[c]);
-                  }
-                }
-                __syncwarp();
-              }
-            }
-#pragma unroll
-            for (int i = 0; i < kTok / 8; ++i) stage8(buf, i, y, i, kTok / 8);
-            close_tokens(buf, &P.mo, P.out, row_j + tok0, ch0, P.M, kTok, nr - tok0, nc);
           }
         }
-        if (!empty_sum) {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(even_addr(&tempty[acc]));
+        // (both blocks take turns: a tile that ends after the first gives the second's turn)
+        if (ncols <= 64 && elect_one()) bulk_commit();
+      } else {
+        const int64_t row = (int64_t)seg_off[r.seg] + row0;
+        const bool up_half = GATED && q >= 2;
+        // this thread's channels: ch0 + lane/4 + 8c
+        float bias[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        if (MODE == kFwd && P.bias != nullptr) {
+          const float* bp = P.bias + (size_t)r.e * P.M * (GATED ? 2 : 1) + (up_half ? P.M : 0) + ch0;
+#pragma unroll
+          for (int c = 0; c < 4; ++c) {
+            const int ch = (lane >> 2) + 8 * c;
+            if (ch < nc) bias[c] = __ldg(bp + ch);
+          }
         }
+        uint32_t next[32];
+        if (half < nchunks) load_block(d + half * 32, next);
+        for (int j = half; j < nchunks; j += 2) {
+          const int64_t row_j = row + j * 32;
+          const int nr = rows - j * 32;
+          // tokens whose results this warp writes: all 32, or gated its half
+          const int tok0 = up_half ? 16 : 0;
+          constexpr int kTok = GATED ? 16 : 32;
+          // the residual's block, on its way while the accumulator is read
+          uint4 res[MODE == kFwd ? kTok / 8 : 1];
+          if constexpr (MODE == kFwd) {
+            if (P.residual != nullptr) {
+              const uint16_t* src = P.residual + (row_j + tok0) * P.M + ch0;
+#pragma unroll
+              for (int i = 0; i < kTok / 8; ++i) {
+                const int rr = i * 8 + frow;
+                res[i] = rr + tok0 < nr && fcol < nc
+                             ? *reinterpret_cast<const uint4*>(src + (size_t)rr * P.M + fcol)
+                             : make_uint4(0, 0, 0, 0);
+              }
+            }
+          }
+          tmem_ld_wait(next);
+          float z[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            z[i] = __uint_as_float(next[i]) + bias[(i >> 4) * 2 + ((i >> 1) & 1)];
+          if (j + 2 < nchunks) load_block(d + (j + 2) * 32, next);
+          if constexpr (MODE == kFwd) {
+            if (P.pre != nullptr) {
+              const int wide = P.M * (GATED ? 2 : 1);
+              uint8_t* buf = open_block();
+#pragma unroll
+              for (int i = 0; i < 4; ++i) stage8(buf, i, z, i, 4);
+              // (a gate half's block may reach into the up half's columns: lane stores)
+              const bool inside = !GATED || up_half || nc >= 32;
+              close_tokens(buf, &P.mp, P.pre, row_j, (up_half ? P.M : 0) + ch0, wide,
+                           inside ? 32 : INT_MAX, nr, nc);
+            }
+          }
+          float y[kTok];  // the results: fragments of kTok / 8 token groups
+          if constexpr (GATED) {
+            // lanes 0..63 of the accumulator are gates, 64..127 the same channels' ups.
+            // The gate's warp takes tokens 0..15, the up's 16..31: each hands the other
+            // its 16 values a thread through a staging block, in fp32.
+            uint64_t* bar = &swap[half * 2 + (q & 1)];
+            uint8_t* buf = open_block();
+            float4* mine = reinterpret_cast<float4*>(buf) + lane;
+            const float4* theirs =
+                reinterpret_cast<const float4*>(epi + ((wid - 4) ^ 2) * 4096 + (buf - blocks)) + lane;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {  // (h, j) = (i / 2, i % 2 of the pair handed over)
+              const int lo = (i >> 1) * 16 + (i & 1) * 4, hi = lo + 8;
+              mine[i * 32] = up_half ? make_float4(z[lo], z[lo + 1], z[lo + 2], z[lo + 3])
+                                     : make_float4(z[hi], z[hi + 1], z[hi + 2], z[hi + 3]);
+            }
+            __syncwarp();
+            if (elect_one()) {
+              bulk_commit();
+              mbar_arrive(bar);
+            }
+            if (!warp_wait(bar, nswap++ & 1u)) {
+              ok = false;
+              break;
+            }
+            float4 other[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) other[i] = theirs[i * 32];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+            if (!warp_wait(bar, nswap++ & 1u)) {
+              ok = false;
+              break;
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int lo = (i >> 1) * 16 + (i & 1) * 4, hi = lo + 8;
+              const float o[4] = {other[i].x, other[i].y, other[i].z, other[i].w};
+#pragma unroll
+              for (int u = 0; u < 4; ++u) {
+                const float g = up_half ? o[u] : z[lo + u], v = up_half ? z[hi + u] : o[u];
+                y[i * 4 + u] = g * sigmoid_f(g) * v;
+              }
+            }
+          } else {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) y[i] = z[i];
+            if (MODE == kFwd) {
+              if (P.act == MOE_ACT_RELU) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] = z[i] < 0.0f ? 0.0f : z[i];
+              } else if (P.act == MOE_ACT_GELU) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] = gelu_f(z[i]);
+              } else if (P.act == MOE_ACT_SILU) {
+#pragma unroll
+                for (int i = 0; i < 32; ++i) y[i] = z[i] * sigmoid_f(z[i]);
+              }
+            }
+          }
+          uint8_t* buf = open_block();
+          if constexpr (MODE == kFwd) {
+            if (P.residual != nullptr) {
+              // through the staging block into the fragments; added in fp32
+#pragma unroll
+              for (int i = 0; i < kTok / 8; ++i) *piece(buf, i * 8 + frow) = res[i];
+              __syncwarp();
+#pragma unroll
+              for (int i = 0; i < kTok / 8; ++i) {
+                uint32_t f[4];
+                ldmatrix_t(smem_addr(buf) + t_addr + i * 512, f);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                  float* at = y + (c >> 1) * (kTok / 2) + 4 * i + (c & 1) * 2;
+                  at[0] += bf16lo(f[c]);
+                  at[1] += bf16hi(f[c]);
+                }
+              }
+              __syncwarp();
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kTok / 8; ++i) stage8(buf, i, y, i, kTok / 8);
+          close_tokens(buf, &P.mo, P.out, row_j + tok0, ch0, P.M, kTok, nr - tok0, nc);
+        }
+      }
+      if (!empty_sum) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(even_addr(&tempty[acc]));
       }
     }
     if (elect_one()) bulk_wait_all();
@@ -868,30 +889,39 @@ cudaError_t make_map(CUtensorMap* map, const void* ptr, int64_t d0, int64_t d1, 
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-constexpr size_t kSmemLimit = 227 * 1024;
-constexpr size_t kSmemStatic = 1024;  // bounds the kernel's static shared memory
-
-template <int MODE, bool GATED>
-cudaError_t launch_gemm(const LaunchEnv& env, GemmParams& P, int64_t max_tiles) {
-  const size_t table = sizeof(int32_t) * ((size_t)P.E * (MODE == kWeights ? 2 : 4) + 1);
-  const size_t smem = kSmemLimit - kSmemStatic;
-  P.ring = (int)((smem - 1024 - epi_bytes(MODE == kWeights) - table) / 1024 * 1024);
-  static_assert(kSmemLimit - kSmemStatic - 1024 - epi_bytes(false) - 17 * 1024 >= 3 * kMaxSlice &&
-                    kSmemLimit - kSmemStatic - 1024 - epi_bytes(true) - 9 * 1024 >= 4 * 32 * 1024,
-                "three of the largest slices, four of the weights gradient's");
-  int per_sm = 1;
-  const auto kernel = expert_gemm_kernel<MODE, GATED>;
-  cudaError_t err = blocks_per_sm((const void*)kernel, kGemmThreads, smem, &per_sm);
-  if (err != cudaSuccess) return err;
-  int64_t pairs = max_tiles < env.num_sms / 2 ? max_tiles : env.num_sms / 2;
-  if (pairs < 1) pairs = 1;
-  return launch_pdl(env, kernel, dim3((unsigned)(2 * pairs)), dim3(kGemmThreads), smem, P);
-}
-
 // Token tiles of `bn` rows there can be at most: full ones, and a partial one
 // for each expert that can hold a row.
 int64_t max_token_tiles(int64_t assignments, int E, int64_t bn) {
   return assignments / bn + (assignments < E ? assignments : E);
+}
+
+constexpr size_t kSmemLimit = 227 * 1024;
+constexpr size_t kSmemStatic = 1024;  // bounds the kernel's static shared memory
+
+template <int MODE, bool GATED>
+cudaError_t launch_gemm(const LaunchEnv& env, GemmParams& P, int64_t max_tiles = 0) {
+  constexpr int kTileM = GATED ? kBM : 2 * kBM;
+  const int64_t all = env.num_sms / 2;
+  if (MODE != kWeights) {
+    const int64_t ct = (P.M + kTileM - 1) / kTileM;
+    max_tiles = max_token_tiles(P.max_rows, P.E, kBN) * ct;
+    // the tiles' height is chosen where there are at most 16 rounds of them
+    P.adapt = max_tiles <= 16 * all;
+    if (P.adapt) max_tiles = max_token_tiles(P.max_rows, P.E, 32) * ct;
+  }
+  const size_t table = sizeof(int32_t) * ((size_t)P.E * (MODE == kWeights ? 2 : 4) + 1);
+  const size_t smem = kSmemLimit - kSmemStatic;
+  P.ring = (int)((smem - 1024 - epi_bytes(MODE == kWeights) - table) / 1024 * 1024);
+  static_assert(kSmemLimit - kSmemStatic - 1024 - epi_bytes(false) - 17 * 1024 >= 5 * kMaxSlice &&
+                    kSmemLimit - kSmemStatic - 1024 - epi_bytes(true) - 9 * 1024 >= 4 * kMaxSlice,
+                "five of the largest slices, four of the weights gradient's");
+  int per_sm = 1;
+  const auto kernel = expert_gemm_kernel<MODE, GATED>;
+  cudaError_t err = blocks_per_sm((const void*)kernel, kGemmThreads, smem, &per_sm);
+  if (err != cudaSuccess) return err;
+  int64_t pairs = max_tiles < all ? max_tiles : all;
+  if (pairs < 1) pairs = 1;
+  return launch_pdl(env, kernel, dim3((unsigned)(2 * pairs)), dim3(kGemmThreads), smem, P);
 }
 
 void segments_of(GemmParams& P, const ExpertMatmul& a) {
@@ -912,7 +942,6 @@ cudaError_t token_operand(GemmParams& P, const ExpertMatmul& a, const void* rows
   }
   P.kdim = cols;
   P.band = 8;
-  P.max_n = 256;
   // ranking costs E^2 / 384 steps a CTA: where tiles are large enough to differ
   P.sorted = a.E > 1 && a.assignments >= (int64_t)32 * a.E;
   return cudaSuccess;
@@ -926,7 +955,7 @@ int wide_features(const ExpertMatmul& a) {
 
 bool expert_tiles_fit(int64_t assignments, int E, int in, int wide) {
   const int64_t ct = (wide + kBM - 1) / kBM, it = (in + kBM - 1) / kBM;
-  const int64_t tt = max_token_tiles(assignments, E, kBN);
+  const int64_t tt = max_token_tiles(assignments, E, 32);
   return tt * (ct > it ? ct : it) < (int64_t(1) << 31) && (int64_t)E * ct * it < (int64_t(1) << 31);
 }
 
@@ -946,9 +975,7 @@ cudaError_t launch_expert_matmul(const LaunchEnv& env, const ExpertMatmul& a) {
   P.pre = static_cast<uint16_t*>(a.pre);
   P.M = a.out_features;
   P.act = a.act;
-  const int64_t tt = max_token_tiles(a.assignments, a.E, kBN);
-  if (gated) return launch_gemm<kFwd, true>(env, P, tt * ((P.M + kBM - 1) / kBM));
-  return launch_gemm<kFwd, false>(env, P, tt * ((P.M + 2 * kBM - 1) / (2 * kBM)));
+  return gated ? launch_gemm<kFwd, true>(env, P) : launch_gemm<kFwd, false>(env, P);
 }
 
 cudaError_t launch_expert_grad_rows(const LaunchEnv& env, const ExpertMatmul& a, const void* dz,
@@ -962,8 +989,7 @@ cudaError_t launch_expert_grad_rows(const LaunchEnv& env, const ExpertMatmul& a,
   if (err != cudaSuccess) return err;
   P.out = static_cast<uint16_t*>(grad_x);
   P.M = a.in_features;
-  const int64_t ct = (P.M + 2 * kBM - 1) / (2 * kBM);
-  return launch_gemm<kRows, false>(env, P, max_token_tiles(a.assignments, a.E, kBN) * ct);
+  return launch_gemm<kRows, false>(env, P);
 }
 
 cudaError_t launch_expert_grad_weights(const LaunchEnv& env, const ExpertMatmul& a, const void* dz,
