@@ -185,7 +185,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   uint8_t* epi = smem + P.ring;
   int32_t* seg_off = reinterpret_cast<int32_t*>(epi + epi_bytes(MODE == kWeights));
   int32_t* seg_rows = seg_off + P.E;
-  // forward / rows: exclusive prefix of token tiles [E+1], and the experts in the
+  // exclusive prefix of token tiles [E+1] (forward / rows), and the experts in the
   // table's order [E]
   int32_t* first = seg_rows + P.E;
   int32_t* expert = first + P.E + 1;
@@ -226,7 +226,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     if (e < P.E) {
       seg[i] = segment(P, e, blockIdx.x == 0);
       my_rows += (unsigned long long)seg[i].rows;
-      if (MODE != kWeights && P.sorted) first[e] = seg[i].rows;
+      if (P.sorted) first[e] = seg[i].rows;
     }
   }
   if (my_rows != 0ull) atomicAdd(&rows_sum, my_rows);
@@ -258,7 +258,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   int at[kMine];
 #pragma unroll
   for (int i = 0; i < kMine; ++i) at[i] = tid + i * kGemmThreads;
-  if (MODE != kWeights && P.sorted) {
+  if (P.sorted) {
     __syncthreads();
 #pragma unroll
     for (int i = 0; i < kMine; ++i) {
@@ -280,10 +280,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     if (e < P.E) {
       seg_off[at[i]] = seg[i].off;
       seg_rows[at[i]] = seg[i].rows;
-      if (MODE != kWeights) {
-        first[at[i]] = (seg[i].rows + height - 1) / height;
-        expert[at[i]] = e;
-      }
+      expert[at[i]] = e;
+      if (MODE != kWeights) first[at[i]] = (seg[i].rows + height - 1) / height;
     }
   }
   tc_fence_before();
@@ -322,8 +320,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     Tile r;
     if constexpr (MODE == kWeights) {
       const int nt = (P.cols + kBN - 1) / kBN;
-      r.e = r.seg = t / (ctiles * nt);
-      const int u = t - r.e * ctiles * nt;
+      r.seg = t / (ctiles * nt);
+      r.e = expert[r.seg];
+      const int u = t - r.seg * ctiles * nt;
       r.c = u / nt;
       r.row0 = (u - r.c * nt) * kBN;  // first column
       r.rows = min(kBN, P.cols - r.row0);
@@ -363,7 +362,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   const int rounds = (total + pairs - 1) / pairs;
   auto my_tile = [&](int j) -> int {
     int t;
-    if (MODE != kWeights && P.sorted) {
+    if (P.sorted) {
       const int round = pair < (pairs >> 1) ? j : rounds - 1 - j;
       t = round * pairs + ((round & 1) ? pairs - 1 - pair : pair);
     } else {
@@ -839,7 +838,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       if (!empty_sum) {
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(even_addr(&tempty[acc]));
+        if (lane == 0) mbar_arrive_remote(even_addr(&tempty[acc]));
       }
     }
     if (elect_one()) bulk_wait_all();
@@ -909,11 +908,11 @@ cudaError_t launch_gemm(const LaunchEnv& env, GemmParams& P, int64_t max_tiles =
     P.adapt = max_tiles <= 16 * all;
     if (P.adapt) max_tiles = max_token_tiles(P.max_rows, P.E, 32) * ct;
   }
-  const size_t table = sizeof(int32_t) * ((size_t)P.E * (MODE == kWeights ? 2 : 4) + 1);
+  const size_t table = sizeof(int32_t) * ((size_t)P.E * 4 + 1);
   const size_t smem = kSmemLimit - kSmemStatic;
   P.ring = (int)((smem - 1024 - epi_bytes(MODE == kWeights) - table) / 1024 * 1024);
   static_assert(kSmemLimit - kSmemStatic - 1024 - epi_bytes(false) - 17 * 1024 >= 5 * kMaxSlice &&
-                    kSmemLimit - kSmemStatic - 1024 - epi_bytes(true) - 9 * 1024 >= 4 * kMaxSlice,
+                    kSmemLimit - kSmemStatic - 1024 - epi_bytes(true) - 17 * 1024 >= 4 * kMaxSlice,
                 "five of the largest slices, four of the weights gradient's");
   int per_sm = 1;
   const auto kernel = expert_gemm_kernel<MODE, GATED>;
@@ -932,6 +931,8 @@ void segments_of(GemmParams& P, const ExpertMatmul& a) {
   P.max_rows = a.assignments;
   P.E = a.E;
   P.capacity = a.capacity;
+  // ranking costs E^2 / 384 steps a CTA: where tiles are large enough to differ
+  P.sorted = a.E > 1 && a.assignments >= (int64_t)32 * a.E;
 }
 
 // The token operand's maps, and the tiles' shape.
@@ -942,8 +943,6 @@ cudaError_t token_operand(GemmParams& P, const ExpertMatmul& a, const void* rows
   }
   P.kdim = cols;
   P.band = 8;
-  // ranking costs E^2 / 384 steps a CTA: where tiles are large enough to differ
-  P.sorted = a.E > 1 && a.assignments >= (int64_t)32 * a.E;
   return cudaSuccess;
 }
 

@@ -151,6 +151,13 @@ __device__ __forceinline__ uint32_t even_addr(const void* p) {
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_addr(p)));
   return r;
 }
+// A plain arrival on a barrier of either CTA: says that accumulator reads are done
+// (ordered by the tcgen05 fence before it).  A release at cluster scope would wait
+// for the thread's global stores as well, 2000 to 3000 cycles of every tile.
+__device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
+}
+// An arrival that publishes this thread's shared-memory writes to the other CTA.
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
   asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
                : "memory");
