@@ -245,10 +245,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       if (lane == 0 && n > 0) atomicAdd(&tiles_at[c], n);
     }
     __syncthreads();
-    int64_t best = INT64_MAX;
+    // (at most 16 rounds at the largest height: everything fits 32 bits)
+    uint32_t best = 0xffffffffu;
     for (int c = 0; c < kHeights; ++c) {
-      const int64_t rounds = ((int64_t)tiles_at[c] * ctiles + pairs - 1) / pairs;
-      const int64_t cost = rounds * slice_cost(kBN - 32 * c);
+      const uint32_t rounds = ((uint32_t)tiles_at[c] * ctiles + pairs - 1) / pairs;
+      const uint32_t cost = rounds * slice_cost(kBN - 32 * c);
       if (cost < best) {
         best = cost;
         height = kBN - 32 * c;
@@ -519,8 +520,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
           const int at = place(head, bytes);
           if (stale_tail(depth, k0)) {
             ok = wait(&fixed[s], (fix_par >> s) & 1u);
-            // the zeros are generic writes of both CTAs: acquired at cluster scope
-            mbar_try_wait_cluster(&fixed[s], (fix_par >> s) & 1u);
             fix_par ^= 1u << s;
           } else {
             ok = wait(&full[s], (full_par >> s) & 1u);
@@ -563,7 +562,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         if (!warp_wait(&landed[s], (par >> s) & 1u)) break;
         par ^= 1u << s;
         zero_stale(smem + at, depth, k0, bytes / 8192);
-        if (lane == 0) mbar_arrive_cluster(even_addr(&fixed[s]));
+        if (lane == 0) mbar_arrive_remote(even_addr(&fixed[s]));
       }
     }
   } else if (wid >= 4) {

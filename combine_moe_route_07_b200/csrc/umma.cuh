@@ -151,29 +151,14 @@ __device__ __forceinline__ uint32_t even_addr(const void* p) {
   asm("mapa.shared::cluster.u32 %0, %1, 0;" : "=r"(r) : "r"(smem_addr(p)));
   return r;
 }
-// A plain arrival on a barrier of either CTA: says that accumulator reads are done
-// (ordered by the tcgen05 fence before it).  A release at cluster scope would wait
-// for the thread's global stores as well, 2000 to 3000 cycles of every tile.
+// A plain arrival on a barrier of either CTA.  What it announces is ordered by the
+// fences before it (accumulator reads by the tcgen05 fence, zeros written for the
+// async proxy by the proxy fence, each complete on its own SM when the thread passes
+// it); a release at cluster scope would wait for the thread's global stores as well,
+// 2000 to 3000 cycles of every tile.
 __device__ __forceinline__ void mbar_arrive_remote(uint32_t addr) {
   asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(addr) : "memory");
 }
-// An arrival that publishes this thread's shared-memory writes to the other CTA.
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t addr) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(addr)
-               : "memory");
-}
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint64_t* bar, uint32_t parity) {
-  uint32_t ok;
-  asm volatile(
-      "{\n .reg .pred p;\n"
-      " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-      " selp.u32 %0, 1, 0, p;\n}"
-      : "=r"(ok)
-      : "r"(smem_addr(bar)), "r"(parity)
-      : "memory");
-  return ok != 0;
-}
-
 // ---- tensor-map copies ------------------------------------------------------
 // Into this CTA's memory, completing on `bar`, a barrier address of either CTA
 // of the pair.  No multicast.
