@@ -554,8 +554,8 @@ size_t moe_expert_matmul_backward_scratch_bytes(const moe_shape_t* shape, int32_
   if (!shape_ok(shape) || src_layout(shape)) return 0;
   if (out_features < 8 || (out_features % 8) != 0 || out_features > 65536) return 0;
   if (act < MOE_ACT_NONE || act > MOE_ACT_SWIGLU) return 0;
-  const int64_t tiles = moe::expert_act_tiles(int64_t(shape->tokens) * shape->k, shape->experts);
-  return size_t(tiles > 0 ? tiles : 1) * wide_of(out_features, act) * sizeof(float);
+  return moe::expert_act_scratch_bytes(int64_t(shape->tokens) * shape->k, shape->experts,
+                                       wide_of(out_features, act));
 }
 
 moe_status_t moe_expert_matmul_backward(const moe_shape_t* shape, int32_t in_features,
@@ -601,8 +601,8 @@ moe_status_t moe_expert_matmul_backward(const moe_shape_t* shape, int32_t in_fea
   const void* dz = act == MOE_ACT_NONE ? grad_out : grad_pre;
   cudaError_t err = cudaSuccess;
   if (act != MOE_ACT_NONE || grad_bias != nullptr)
-    err = moe::launch_expert_act_backward(env, a, grad_out, pre, grad_pre,
-                                          static_cast<float*>(scratch), grad_bias);
+    err = moe::launch_expert_act_backward(env, a, grad_out, pre, grad_pre, scratch,
+                                          grad_bias);
   if (err == cudaSuccess && grad_x != nullptr)
     err = moe::launch_expert_grad_rows(env, a, dz, grad_x);
   if (err == cudaSuccess && grad_w != nullptr)

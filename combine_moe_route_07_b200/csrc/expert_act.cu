@@ -28,6 +28,7 @@ struct ActParams {
   const uint16_t* z;
   uint16_t* dz;      // NULL: dz is dy itself
   float* partial;    // [tiles][W] or NULL
+  int32_t* tile_of;  // with partial: first tile of each expert [E+1]
   const int32_t* counts;
   const int32_t* off;
   WsHeader* hdr;
@@ -99,7 +100,7 @@ __device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
 constexpr int kUnroll = 2;  // rows of a warp whose loads are in flight together
 
 template <int ACT>
-__global__ void __launch_bounds__(kThreads)
+__global__ void __launch_bounds__(kThreads, 4)
     expert_act_backward_kernel(ActParams P) {
   extern __shared__ int32_t tab[];
   __shared__ float red[kWarps][2][256];
@@ -132,6 +133,8 @@ __global__ void __launch_bounds__(kThreads)
     if (threadIdx.x == 0 && blockIdx.x == 0) report(P.hdr, MOE_ERR_DEVICE_RANGE, P.E);
     tiles = 0;
   }
+  if (P.partial != nullptr && blockIdx.x == 0)
+    for (int e = threadIdx.x; e <= P.E; e += kThreads) P.tile_of[e] = tiles > 0 ? first[e] : 0;
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int strips = (P.F + 255) / 256;  // 256 channels: 8 a lane
   constexpr bool gated = ACT == MOE_ACT_SWIGLU, plain = ACT == MOE_ACT_NONE;
@@ -219,54 +222,45 @@ __global__ void __launch_bounds__(kThreads)
   }
 }
 
-// grad_bias[e][c] = sum of expert e's partial sums: 8 warps take every 8th
-// tile, then meet in warp order.  One CTA for 32 channels of one expert.
-__global__ void __launch_bounds__(kThreads) expert_bias_reduce_kernel(ActParams P, float* grad_bias) {
-  __shared__ int32_t red_i[kWarps];
-  __shared__ int first_s;
-  __shared__ float red[kWarps][32];
-  __shared__ unsigned long long rows_sum;
-  if (threadIdx.x == 0) rows_sum = 0ull;
-  __syncthreads();
+// grad_bias[e][c] = sum of expert e's partial sums: 8 warps take every 8th tile,
+// then meet in warp order.  One CTA for 128 channels of one expert, four a lane.
+__global__ void __launch_bounds__(kThreads)
+    expert_bias_reduce_kernel(const float* __restrict__ partial, const int32_t* __restrict__ tile_of,
+                              int W, float* __restrict__ grad_bias) {
+  __shared__ float4 red[kWarps][32];
   pdl_wait();
   pdl_trigger();
   const int e = blockIdx.y, lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-  // tiles of the experts before e, and the rows of all
-  int before = 0;
-  unsigned long long my_rows = 0ull;
-  for (int i = threadIdx.x; i < P.E; i += kThreads) {
-    int o;
-    const int r = seg_rows(P, i, &o);
-    my_rows += (unsigned long long)r;
-    if (i < e) before += (r + kActRows - 1) / kActRows;
-  }
-  if (my_rows != 0ull) atomicAdd(&rows_sum, my_rows);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) before += __shfl_xor_sync(kFull, before, o);
-  if (lane == 0) red_i[w] = before;
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    int s = 0;
-    for (int i = 0; i < kWarps; ++i) s += red_i[i];
-    first_s = s;
-  }
-  __syncthreads();
-  int o;
-  const int tiles = (seg_rows(P, e, &o) + kActRows - 1) / kActRows;
-  const int c = blockIdx.x * 32 + lane;
-  float s = 0.0f;
-  if (c < P.W && (int64_t)rows_sum <= P.max_rows) {
-    const float* p = P.partial + (size_t)first_s * P.W + c;
+  const int c = blockIdx.x * 128 + lane * 4;
+  const int lo = __ldg(tile_of + e), hi = __ldg(tile_of + e + 1);
+  float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  if (c < W) {
 #pragma unroll 4
-    for (int i = w; i < tiles; i += kWarps) s += __ldg(p + (size_t)i * P.W);
+    for (int i = lo + w; i < hi; i += kWarps) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(partial + (size_t)i * W + c));
+      s.x += v.x;
+      s.y += v.y;
+      s.z += v.z;
+      s.w += v.w;
+    }
   }
   red[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < P.W) {
-    float a = 0.0f;
+  if (w == 0 && c < W) {
+    float4 a = red[0][lane];
 #pragma unroll
-    for (int i = 0; i < kWarps; ++i) a += red[i][lane];
-    grad_bias[(size_t)e * P.W + c] = a;
+    for (int i = 1; i < kWarps; ++i) {
+      const float4 v = red[i][lane];
+      a.x += v.x;
+      a.y += v.y;
+      a.z += v.z;
+      a.w += v.w;
+    }
+    float* out = grad_bias + (size_t)e * W + c;
+    out[0] = a.x;
+    out[1] = a.y;
+    out[2] = a.z;
+    out[3] = a.w;
   }
 }
 
@@ -276,13 +270,23 @@ int64_t expert_act_tiles(int64_t assignments, int E) {
   return assignments / kActRows + (assignments < E ? assignments : E);
 }
 
+size_t expert_act_scratch_bytes(int64_t assignments, int E, int wide) {
+  // the experts' first tiles, then the tiles' sums
+  const int64_t tiles = expert_act_tiles(assignments, E);
+  return (((size_t)E + 1) * sizeof(int32_t) + 15) / 16 * 16 + (size_t)tiles * wide * sizeof(float);
+}
+
 cudaError_t launch_expert_act_backward(const LaunchEnv& env, const ExpertMatmul& a, const void* dy,
-                                       const void* z, void* dz, float* partial, float* grad_bias) {
+                                       const void* z, void* dz, void* scratch, float* grad_bias) {
   ActParams P = {};
   P.dy = static_cast<const uint16_t*>(dy);
   P.z = static_cast<const uint16_t*>(z);
   P.dz = static_cast<uint16_t*>(dz);
-  P.partial = grad_bias != nullptr ? partial : nullptr;
+  if (grad_bias != nullptr) {
+    P.tile_of = static_cast<int32_t*>(scratch);
+    P.partial = reinterpret_cast<float*>(static_cast<char*>(scratch) +
+                                         (((size_t)a.E + 1) * sizeof(int32_t) + 15) / 16 * 16);
+  }
   P.counts = a.counts;
   P.off = a.expert_off;
   P.hdr = a.hdr;
@@ -309,8 +313,9 @@ cudaError_t launch_expert_act_backward(const LaunchEnv& env, const ExpertMatmul&
   if (grid < 1) grid = 1;
   err = launch_pdl(env, kernel, dim3((unsigned)grid), dim3(kThreads), smem, P);
   if (err != cudaSuccess || grad_bias == nullptr) return err;
-  return launch_pdl(env, expert_bias_reduce_kernel, dim3((unsigned)((P.W + 31) / 32), (unsigned)P.E),
-                    dim3(kThreads), 0, P, grad_bias);
+  return launch_pdl(env, expert_bias_reduce_kernel,
+                    dim3((unsigned)((P.W + 127) / 128), (unsigned)P.E), dim3(kThreads), 0,
+                    (const float*)P.partial, (const int32_t*)P.tile_of, P.W, grad_bias);
 }
 
 }  // namespace moe

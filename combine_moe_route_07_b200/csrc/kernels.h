@@ -231,8 +231,9 @@ cudaError_t launch_expert_grad_weights(const LaunchEnv& env, const ExpertMatmul&
 // Rows of a tile of the activation's gradient, and the most tiles there can be.
 constexpr int kActRows = 64;
 int64_t expert_act_tiles(int64_t assignments, int E);
+size_t expert_act_scratch_bytes(int64_t assignments, int E, int wide);
 cudaError_t launch_expert_act_backward(const LaunchEnv& env, const ExpertMatmul& a, const void* dy,
-                                       const void* z, void* dz, float* partial, float* grad_bias);
+                                       const void* z, void* dz, void* scratch, float* grad_bias);
 
 // sparse: most slots may be dropped (capacity mode)
 cudaError_t launch_combine(const LaunchEnv& env, const void* y, const int32_t* dst_pos,
