@@ -29,6 +29,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 from typing import Optional
 
 import torch
@@ -64,11 +65,15 @@ class MoeShape:
         return ((MOE_F_RENORM if self.renorm else 0) | (MOE_F_FP8 if self.fp8 else 0)
                 | (MOE_F_SRC_LAYOUT if self.src_layout else 0))
 
-    def c(self) -> _binding.MoeShapeC:
+    @functools.cached_property
+    def _c(self) -> _binding.MoeShapeC:
         return _binding.MoeShapeC(self.tokens, self.hidden, self.experts, self.k, self.ranks,
                                   self.capacity, self.align, self.flags)
 
-    @property
+    def c(self) -> _binding.MoeShapeC:
+        return self._c
+
+    @functools.cached_property
     def rows(self) -> int:
         return moe_layout_rows(self)
 
@@ -100,7 +105,7 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, shape=None) -> Option
         raise ValueError(f"{name} must be contiguous")
     if dtype is not None and t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if shape is not None and tuple(t.shape) != tuple(shape):
+    if shape is not None and t.shape != shape:
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -410,30 +415,20 @@ def moe_combine(shape: MoeShape, y: torch.Tensor, dst_pos: torch.Tensor, gates: 
     return out
 
 
-class _On:
-    """The device of a call: its index, and a guard that makes it current for
-    the launch where it is not already."""
-
-    def __init__(self, ws: Workspace, *tensors):
-        self.device = ws.buf.device
-        for t in tensors:
-            if t is not None and t.device != self.device:
-                raise ValueError(f"every tensor must be on the workspace's device {self.device}, "
-                                 f"got {t.device}")
-
-    def __enter__(self):
-        index = self.device.index
-        self.before = torch.cuda.current_device()
-        if index != self.before:
-            torch.cuda.set_device(index)
-        else:
-            self.before = None
-        return torch.cuda.current_stream(index).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.before is not None:
-            torch.cuda.set_device(self.before)
-        return False
+def _run(what: str, ws: Workspace, tensors, call):
+    """call(stream) on the workspace's device, which every tensor must be on; that
+    device is made current for the launch where it is not already."""
+    dev = ws.buf.device
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"every tensor must be on the workspace's device {dev}, got {t.device}")
+    if dev.index == torch.cuda.current_device():
+        st = call(_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = call(_stream(dev))
+    if st != _binding.MOE_OK:
+        raise MoeError(st, what)
 
 
 @dataclasses.dataclass(frozen=True)
@@ -448,11 +443,15 @@ class ScoreRule:
     group_top: int = 1
     scale: float = 1.0
 
-    def c(self) -> _binding.MoeScoreC:
+    @functools.cached_property
+    def _c(self) -> _binding.MoeScoreC:
         if self.func not in _binding.MOE_SCORES:
             raise ValueError(f"func must be one of {sorted(_binding.MOE_SCORES)}, got {self.func!r}")
         return _binding.MoeScoreC(_binding.MOE_SCORES[self.func], self.groups, self.top_groups,
                                   self.group_top, self.scale)
+
+    def c(self) -> _binding.MoeScoreC:
+        return self._c
 
 
 def moe_route_scored(shape: MoeShape, logits: torch.Tensor, rule: ScoreRule,
@@ -466,13 +465,12 @@ def moe_route_scored(shape: MoeShape, logits: torch.Tensor, rule: ScoreRule,
         ids = torch.empty((T, k), dtype=torch.int32, device=dev)
     if gates is None:
         gates = torch.empty((T, k), dtype=torch.float32, device=dev)
-    with _On(ws, logits, bias, ids, gates) as stream:
-        st = _binding.lib().moe_route_scored(
-            ctypes.byref(shape.c()), _ptr(logits, "logits", torch.float32, (T, E)),
-            _ptr(bias, "bias", torch.float32, (E,)), ctypes.byref(rule.c()),
-            _ptr(ids, "ids", torch.int32, (T, k)), _ptr(gates, "gates", torch.float32, (T, k)),
-            ws.ptr, ws.nbytes, stream)
-    _check(st, "moe_route_scored")
+    _run("moe_route_scored", ws, (logits, bias, ids, gates),
+         lambda stream: _binding.lib().moe_route_scored(
+             ctypes.byref(shape.c()), _ptr(logits, "logits", torch.float32, (T, E)),
+             _ptr(bias, "bias", torch.float32, (E,)), ctypes.byref(rule.c()),
+             _ptr(ids, "ids", torch.int32, (T, k)), _ptr(gates, "gates", torch.float32, (T, k)),
+             ws.ptr, ws.nbytes, stream))
     return ids, gates
 
 
@@ -483,13 +481,12 @@ def moe_route_scored_backward(shape: MoeShape, logits: torch.Tensor, rule: Score
     T, E, k = shape.tokens, shape.experts, shape.k
     if grad_logits is None:
         grad_logits = torch.empty((T, E), dtype=torch.float32, device=logits.device)
-    with _On(ws, logits, ids, grad_gates, grad_logits) as stream:
-        st = _binding.lib().moe_route_scored_backward(
-            ctypes.byref(shape.c()), _ptr(logits, "logits", torch.float32, (T, E)),
-            ctypes.byref(rule.c()), _ptr(ids, "ids", torch.int32, (T, k)),
-            _ptr(grad_gates, "grad_gates", torch.float32, (T, k)),
-            _ptr(grad_logits, "grad_logits", torch.float32, (T, E)), ws.ptr, ws.nbytes, stream)
-    _check(st, "moe_route_scored_backward")
+    _run("moe_route_scored_backward", ws, (logits, ids, grad_gates, grad_logits),
+         lambda stream: _binding.lib().moe_route_scored_backward(
+             ctypes.byref(shape.c()), _ptr(logits, "logits", torch.float32, (T, E)),
+             ctypes.byref(rule.c()), _ptr(ids, "ids", torch.int32, (T, k)),
+             _ptr(grad_gates, "grad_gates", torch.float32, (T, k)),
+             _ptr(grad_logits, "grad_logits", torch.float32, (T, E)), ws.ptr, ws.nbytes, stream))
     return grad_logits
 
 
@@ -530,15 +527,14 @@ def moe_expert_matmul(shape: MoeShape, x: torch.Tensor, w: torch.Tensor,
     bf16 = torch.bfloat16
     if out is None:
         out = torch.empty((N, F), dtype=bf16, device=x.device)
-    with _On(ws, x, w, counts, expert_off, bias, residual, out, pre) as stream:
-        st = _binding.lib().moe_expert_matmul(
-            ctypes.byref(shape.c()), K, F, a, _ptr(x, "x", bf16, (N, K)), _ptr(w, "w", bf16),
-            _ptr(bias, "bias", torch.float32, (E, wide)),
-            _ptr(counts, "counts", torch.int32, (E,)),
-            _ptr(expert_off, "expert_off", torch.int32, (E + 1,)),
-            _ptr(residual, "residual", bf16, (N, F)), _ptr(out, "out", bf16, (N, F)),
-            _ptr(pre, "pre", bf16, (N, wide)), ws.ptr, ws.nbytes, stream)
-    _check(st, "moe_expert_matmul")
+    _run("moe_expert_matmul", ws, (x, w, counts, expert_off, bias, residual, out, pre),
+         lambda stream: _binding.lib().moe_expert_matmul(
+             ctypes.byref(shape.c()), K, F, a, _ptr(x, "x", bf16, (N, K)), _ptr(w, "w", bf16),
+             _ptr(bias, "bias", torch.float32, (E, wide)),
+             _ptr(counts, "counts", torch.int32, (E,)),
+             _ptr(expert_off, "expert_off", torch.int32, (E + 1,)),
+             _ptr(residual, "residual", bf16, (N, F)), _ptr(out, "out", bf16, (N, F)),
+             _ptr(pre, "pre", bf16, (N, wide)), ws.ptr, ws.nbytes, stream))
     return out
 
 
@@ -578,22 +574,21 @@ def moe_expert_matmul_backward(shape: MoeShape, grad_out: torch.Tensor, x: torch
     elif grad_pre is None:
         grad_pre = torch.empty((N, wide), dtype=bf16, device=dev)
     scratch, nbytes = None, 0
-    cs = shape.c()
-    with _On(ws, grad_out, x, w, counts, expert_off, pre, grad_pre, grad_x, grad_w,
-             grad_bias) as stream:
-        if grad_bias is not None:
-            nbytes = _binding.lib().moe_expert_matmul_backward_scratch_bytes(ctypes.byref(cs), F, a)
-            scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
-        st = _binding.lib().moe_expert_matmul_backward(
-            ctypes.byref(cs), K, F, a, _ptr(grad_out, "grad_out", bf16, (N, F)),
-            _ptr(x, "x", bf16, (N, K)), _ptr(w, "w", bf16), _ptr(pre, "pre", bf16, (N, wide)),
-            _ptr(counts, "counts", torch.int32, (E,)),
-            _ptr(expert_off, "expert_off", torch.int32, (E + 1,)),
-            _ptr(grad_pre, "grad_pre", bf16, (N, wide)), _ptr(grad_x, "grad_x", bf16, (N, K)),
-            _ptr(grad_w, "grad_w", bf16, (E, wide, K)),
-            _ptr(grad_bias, "grad_bias", torch.float32, (E, wide)),
-            None if scratch is None else scratch.data_ptr(), nbytes, ws.ptr, ws.nbytes, stream)
-    _check(st, "moe_expert_matmul_backward")
+    if grad_bias is not None:
+        nbytes = _binding.lib().moe_expert_matmul_backward_scratch_bytes(ctypes.byref(shape.c()),
+                                                                         F, a)
+        scratch = torch.empty(nbytes, dtype=torch.uint8, device=dev)
+    _run("moe_expert_matmul_backward", ws,
+         (grad_out, x, w, counts, expert_off, pre, grad_pre, grad_x, grad_w, grad_bias),
+         lambda stream: _binding.lib().moe_expert_matmul_backward(
+             ctypes.byref(shape.c()), K, F, a, _ptr(grad_out, "grad_out", bf16, (N, F)),
+             _ptr(x, "x", bf16, (N, K)), _ptr(w, "w", bf16), _ptr(pre, "pre", bf16, (N, wide)),
+             _ptr(counts, "counts", torch.int32, (E,)),
+             _ptr(expert_off, "expert_off", torch.int32, (E + 1,)),
+             _ptr(grad_pre, "grad_pre", bf16, (N, wide)), _ptr(grad_x, "grad_x", bf16, (N, K)),
+             _ptr(grad_w, "grad_w", bf16, (E, wide, K)),
+             _ptr(grad_bias, "grad_bias", torch.float32, (E, wide)),
+             None if scratch is None else scratch.data_ptr(), nbytes, ws.ptr, ws.nbytes, stream))
     return ExpertGrads(grad_x, grad_w, grad_bias, grad_pre)
 
 
@@ -611,14 +606,13 @@ def moe_combine_backward(shape: MoeShape, grad_out: torch.Tensor, y: torch.Tenso
         grad_y = torch.empty((N, H), dtype=torch.bfloat16, device=y.device)
     if grad_gates is None:
         grad_gates = torch.empty((T, k), dtype=torch.float32, device=y.device)
-    with _On(ws, grad_out, y, dst_pos, gates, grad_y, grad_gates) as stream:
-        st = _binding.lib().moe_combine_backward(
-            ctypes.byref(shape.c()), _ptr(grad_out, "grad_out", torch.bfloat16, (T, H)),
-            _ptr(y, "y", torch.bfloat16, (N, H)), _ptr(dst_pos, "dst_pos", torch.int32, (T, k)),
-            _ptr(gates, "gates", torch.float32, (T, k)),
-            _ptr(grad_y, "grad_y", torch.bfloat16, (N, H)),
-            _ptr(grad_gates, "grad_gates", torch.float32, (T, k)), ws.ptr, ws.nbytes, stream)
-    _check(st, "moe_combine_backward")
+    _run("moe_combine_backward", ws, (grad_out, y, dst_pos, gates, grad_y, grad_gates),
+         lambda stream: _binding.lib().moe_combine_backward(
+             ctypes.byref(shape.c()), _ptr(grad_out, "grad_out", torch.bfloat16, (T, H)),
+             _ptr(y, "y", torch.bfloat16, (N, H)), _ptr(dst_pos, "dst_pos", torch.int32, (T, k)),
+             _ptr(gates, "gates", torch.float32, (T, k)),
+             _ptr(grad_y, "grad_y", torch.bfloat16, (N, H)),
+             _ptr(grad_gates, "grad_gates", torch.float32, (T, k)), ws.ptr, ws.nbytes, stream))
     return grad_y, grad_gates
 
 

@@ -511,117 +511,149 @@ __global__ void __launch_bounds__(kScoredWarps * 32, scored_min_blocks(NK))
 
 constexpr int kBackWarps = 8;
 
-// One warp per token.  The row of grad_logits is built in shared memory and
-// written once: it is zero outside the chosen experts except with the full
-// softmax.  Store-bound: 4E bytes a token.
+// The sum, or largest value, over the W lanes of a token.
+template <int W>
+__device__ __forceinline__ float lanes_sum(float v) {
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
+  return v;
+}
+template <int W>
+__device__ __forceinline__ float lanes_max(float v) {
+#pragma unroll
+  for (int o = W / 2; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor_sync(kFull, v, o));
+  return v;
+}
+
+// An expert that appears in several slots of a token gets the sum of their parts, in
+// slot order, from its first slot (the others' expert becomes -1).
+template <int W>
+__device__ __forceinline__ float merge_slots(float d, int& e, int lane) {
+  const unsigned same = __match_any_sync(kFull, e < 0 ? -1 - lane : (e | (lane / W) << 16));
+  if (__any_sync(kFull, __popc(same) > 1)) {
+    float sum = 0.0f;
+    for (int j = 0; j < 32; ++j) {
+      const float dj = __shfl_sync(kFull, d, j);
+      if ((same >> j) & 1u) sum += dj;
+    }
+    d = sum;
+    if (lane != __ffs(same) - 1) e = -1;
+  }
+  return d;
+}
+
+// The gradient lives on the chosen experts alone (every rule but the full softmax).
+// W lanes a token, two tokens a warp where k <= 16.  The row is zeroed by wide stores
+// that wait for nothing, the k values follow them (the warp's stores are ordered by
+// the barrier between): store-bound, 4E bytes a token.
+template <int W>
 __global__ void __launch_bounds__(kBackWarps * 32)
     route_scored_backward_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids,
                                  const float* __restrict__ grad_gates, int T, int E, int k,
-                                 ScoreRule R, float* __restrict__ grad_logits, int vec,
-                                 WsHeader* hdr) {
+                                 const __grid_constant__ ScoreRule R,
+                                 float* __restrict__ grad_logits, int vec, WsHeader* hdr) {
+  constexpr int kTok = 32 / W;
+  pdl_wait();
+  pdl_trigger();
+  const int lane = threadIdx.x & 31, j = lane % W;
+  const int step = gridDim.x * kBackWarps * kTok;
+  for (int t0 = (blockIdx.x * kBackWarps + (threadIdx.x >> 5)) * kTok; t0 < T; t0 += step) {
+    const int t = t0 + lane / W;
+    int e = -1;
+    float up = 0.0f;
+    if (j < k && t < T) {
+      e = __ldg(ids + (size_t)t * k + j);
+      up = __ldg(grad_gates + (size_t)t * k + j);
+    }
+    float* out = grad_logits + (size_t)t0 * E;
+    const int n = (min(T - t0, kTok)) * E;
+    if (vec) {
+      for (int i = lane * 4; i < n; i += 128)
+        *reinterpret_cast<float4*>(out + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    } else {
+      for (int i = lane; i < n; i += 32) out[i] = 0.0f;
+    }
+    if (e >= E || (e < 0 && j < k && t < T)) {
+      report(hdr, MOE_ERR_DEVICE_RANGE, e);
+      e = -1;
+    }
+    const float l = e >= 0 ? __ldg(logits + (size_t)t * E + e) : 0.0f;
+    up = e >= 0 ? (float)((double)up * R.scale) : 0.0f;
+    float d;
+    if (R.softmax) {  // renormalised: the softmax of the chosen
+      const float m = lanes_max<W>(e >= 0 ? l : -INFINITY);
+      const float x = e >= 0 ? expf(l - m) : 0.0f;
+      const float p = x * (1.0f / lanes_sum<W>(x));
+      d = p * (up - lanes_sum<W>(up * p));
+    } else {
+      // sigmoid(l) and 1 - sigmoid(l), both without cancellation
+      const float x = expf(-fabsf(l));
+      const float big = 1.0f / (1.0f + x), small = x * big;
+      const float s = e >= 0 ? (l >= 0.0f ? big : small) : 0.0f, c = l >= 0.0f ? small : big;
+      d = up;
+      if (R.renorm) {
+        const float sum = lanes_sum<W>(s), us = lanes_sum<W>(up * s);
+        d = sum > 0.0f ? (up - us / sum) / sum : 0.0f;
+      }
+      d = e >= 0 ? d * s * c : 0.0f;
+    }
+    d = merge_slots<W>(d, e, lane);
+    __syncwarp();
+    if (e >= 0) grad_logits[(size_t)t * E + e] = d;
+  }
+}
+
+// The full softmax without renormalisation: every logit has a gradient.  One warp per
+// token; the row's exponentials stay in shared memory between the passes.
+__global__ void __launch_bounds__(kBackWarps * 32)
+    route_softmax_backward_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids,
+                                  const float* __restrict__ grad_gates, int T, int E, int k,
+                                  double scale, float* __restrict__ grad_logits, int vec,
+                                  WsHeader* hdr) {
   extern __shared__ float4 sback[];
   pdl_wait();
   pdl_trigger();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   const int words = (E + 3) / 4 * 4;
   float* srow = reinterpret_cast<float*>(sback) + (size_t)w * words;
-  const bool dense = R.softmax && !R.renorm;
   for (int t = blockIdx.x * kBackWarps + w; t < T; t += gridDim.x * kBackWarps) {
     const float* row = logits + (size_t)t * E;
     int e = -1;
     float up = 0.0f;
     if (lane < k) {
       e = __ldg(ids + (size_t)t * k + lane);
-      up = (float)((double)__ldg(grad_gates + (size_t)t * k + lane) * R.scale);
+      up = (float)((double)__ldg(grad_gates + (size_t)t * k + lane) * scale);
       if ((unsigned)e >= (unsigned)E) {
         report(hdr, MOE_ERR_DEVICE_RANGE, e);
         e = -1;
-        up = 0.0f;
       }
     }
-    float d = 0.0f;    // this slot's part of the gradient at its expert
-    float dot = 0.0f;  // dense: sum of up * p over the chosen
-    float m = 0.0f, inv = 1.0f;
-    if (R.softmax) {
-      // the maximum and the sum over all experts (dense) or the chosen ones
-      m = -INFINITY;
-      if (dense) {
-        for (int i = lane; i < E; i += 32) {
-          const float l = __ldg(row + i);
-          srow[i] = l;
-          m = fmaxf(m, l);
-        }
-      } else if (e >= 0) {
-        m = __ldg(row + e);
-      }
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
-      float sum = 0.0f;
-      if (dense) {
-        for (int i = lane; i < E; i += 32) {
-          const float p = expf(srow[i] - m);
-          srow[i] = p;
-          sum += p;
-        }
-        __syncwarp();
-      } else if (e >= 0) {
-        sum = expf(__ldg(row + e) - m);
-      }
-      const float own = sum;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-      inv = 1.0f / sum;
-      const float p = dense ? (e >= 0 ? srow[e] * inv : 0.0f) : own * inv;
-      dot = up * p;
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) dot += __shfl_xor_sync(kFull, dot, o);
-      d = dense ? up * p : p * (up - dot);
-      __syncwarp();
-    } else {
-      float s = 0.0f, c = 0.0f;  // sigmoid(l) and 1 - sigmoid(l), both without cancellation
-      if (e >= 0) {
-        const float l = __ldg(row + e);
-        const float x = expf(-fabsf(l));
-        const float big = 1.0f / (1.0f + x), small = x * big;
-        s = l >= 0.0f ? big : small;
-        c = l >= 0.0f ? small : big;
-      }
-      d = up;
-      if (R.renorm) {
-        float sum = s, us = up * s;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) {
-          sum += __shfl_xor_sync(kFull, sum, o);
-          us += __shfl_xor_sync(kFull, us, o);
-        }
-        d = sum > 0.0f ? (up - us / sum) / sum : 0.0f;
-      }
-      d = e >= 0 ? d * s * c : 0.0f;
+    float m = -INFINITY;
+    for (int i = lane; i < E; i += 32) {
+      const float l = __ldg(row + i);
+      srow[i] = l;
+      m = fmaxf(m, l);
     }
-    // an expert that appears in several slots gets the sum of their parts, in
-    // slot order, from its first slot
-    const unsigned same = __match_any_sync(kFull, e);
-    if (__any_sync(kFull, e >= 0 && __popc(same) > 1)) {
-      float sum = 0.0f;
-      for (int j = 0; j < k; ++j) {
-        const float dj = __shfl_sync(kFull, d, j);
-        if ((same >> j) & 1u) sum += dj;
-      }
-      d = sum;
-      if (lane != __ffs(same) - 1) e = -1;
+    m = lanes_max<32>(m);
+    float sum = 0.0f;
+    for (int i = lane; i < E; i += 32) {
+      const float p = expf(srow[i] - m);
+      srow[i] = p;
+      sum += p;
     }
-    if (dense) {
-      for (int i = lane; i < E; i += 32) srow[i] = -(srow[i] * inv) * dot;
-    } else {
-      for (int i = lane; i < E; i += 32) srow[i] = 0.0f;
-    }
+    __syncwarp();
+    const float inv = 1.0f / lanes_sum<32>(sum);
+    float d = e >= 0 ? up * (srow[e] * inv) : 0.0f;
+    const float dot = lanes_sum<32>(d);  // sum of up * p over the chosen
+    d = merge_slots<32>(d, e, lane);
+    for (int i = lane; i < E; i += 32) srow[i] = -(srow[i] * inv) * dot;
     __syncwarp();
     if (e >= 0) srow[e] += d;
     __syncwarp();
     float* out = grad_logits + (size_t)t * E;
     if (vec) {
       for (int i = lane; i < E / 4; i += 32)
-        __stcs(reinterpret_cast<float4*>(out) + i, reinterpret_cast<const float4*>(srow)[i]);
+        reinterpret_cast<float4*>(out)[i] = reinterpret_cast<const float4*>(srow)[i];
     } else {
       for (int i = lane; i < E; i += 32) out[i] = srow[i];
     }
@@ -683,16 +715,24 @@ cudaError_t launch_route_scored_backward(const LaunchEnv& env, const float* logi
                                          const int32_t* ids, const float* grad_gates, int T, int E,
                                          int k, const ScoreRule& rule, float* grad_logits,
                                          WsHeader* hdr) {
-  const size_t smem = sizeof(float) * kBackWarps * (size_t)((E + 3) / 4 * 4);
-  int per_sm = 1;
-  cudaError_t err =
-      blocks_per_sm((const void*)route_scored_backward_kernel, kBackWarps * 32, smem, &per_sm);
-  if (err != cudaSuccess) return err;
-  int64_t grid = ((int64_t)T + kBackWarps - 1) / kBackWarps;
-  if (grid > (int64_t)per_sm * env.num_sms) grid = (int64_t)per_sm * env.num_sms;
   const int vec = (E % 4) == 0 && (reinterpret_cast<uintptr_t>(grad_logits) % 16) == 0;
-  return launch_pdl(env, route_scored_backward_kernel, dim3((unsigned)grid), dim3(kBackWarps * 32),
-                    smem, logits, ids, grad_gates, T, E, k, rule, grad_logits, vec, hdr);
+  const bool dense = rule.softmax && !rule.renorm;
+  const size_t smem = dense ? sizeof(float) * kBackWarps * (size_t)((E + 3) / 4 * 4) : 0;
+  const auto chosen = k <= 16 ? route_scored_backward_kernel<16> : route_scored_backward_kernel<32>;
+  int per_sm = 1;
+  cudaError_t err = blocks_per_sm(
+      dense ? (const void*)route_softmax_backward_kernel : (const void*)chosen, kBackWarps * 32, smem,
+      &per_sm);
+  if (err != cudaSuccess) return err;
+  const int64_t tokens = kBackWarps * (!dense && k <= 16 ? 2 : 1);
+  int64_t grid = ((int64_t)T + tokens - 1) / tokens;
+  if (grid > (int64_t)per_sm * env.num_sms) grid = (int64_t)per_sm * env.num_sms;
+  if (dense)
+    return launch_pdl(env, route_softmax_backward_kernel, dim3((unsigned)grid),
+                      dim3(kBackWarps * 32), smem, logits, ids, grad_gates, T, E, k, rule.scale,
+                      grad_logits, vec, hdr);
+  return launch_pdl(env, chosen, dim3((unsigned)grid), dim3(kBackWarps * 32), 0, logits, ids,
+                    grad_gates, T, E, k, rule, grad_logits, vec, hdr);
 }
 
 }  // namespace moe
