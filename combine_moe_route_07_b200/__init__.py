@@ -92,8 +92,15 @@ def moe_workspace_bytes(shape: MoeShape) -> int:
     return int(n)
 
 
+# The current stream's handle without building a torch.cuda.Stream (2 us of a call
+# that takes 8); torch builds without it go through the object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device=None) -> int:
-    return torch.cuda.current_stream(device).cuda_stream
+    if _raw_stream is None or not isinstance(device, torch.device):
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream(torch.cuda.current_device() if device.index is None else device.index)
 
 
 def _ptr(t: Optional[torch.Tensor], name: str, dtype=None, shape=None) -> Optional[int]:
