@@ -47,7 +47,9 @@ constexpr int kGemmThreads = (4 + kEpiWarps) * 32;
 constexpr int epi_bytes(bool weights) { return kEpiWarps * (weights ? 8192 : 4096); }
 constexpr int kMaxSlice = kABytes + 128 * kBK * 2;
 constexpr int kTmemCols = 512;
-constexpr uint64_t kWaitNs = 2000000000ull;
+// The longest wait: two seconds, and 20 ns for each row (the weights gradient of one
+// expert is one tile's contraction over all its rows: about 6 ns a row).
+constexpr uint64_t kWaitNs = 2000000000ull, kWaitRowNs = 20ull;
 
 enum { kFwd = 0, kRows = 1, kWeights = 2 };
 
@@ -146,7 +148,7 @@ __device__ __forceinline__ int box_rows(int half) { return (half + 31) & ~31; }
 // The part of a wait that is not over at once; false: it gave up, or another
 // role of this CTA did.
 __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, int* abort_flag,
-                                       WsHeader* hdr) {
+                                       uint64_t limit_ns, WsHeader* hdr) {
   volatile int* stop = abort_flag;
   uint64_t t0 = 0;
   for (unsigned it = 1; it < (1u << 24); ++it) {
@@ -154,7 +156,7 @@ __device__ __noinline__ bool wait_long(uint64_t* bar, uint32_t parity, int* abor
     if ((it & 63u) == 0u) {
       const uint64_t now = global_ns();
       if (t0 == 0) t0 = now;
-      if (*stop != 0 || now - t0 > kWaitNs) break;
+      if (*stop != 0 || now - t0 > limit_ns) break;
     }
   }
   if (*stop == 0) report(hdr, MOE_ERR_DEVICE_TIMEOUT, blockIdx.x);
@@ -309,7 +311,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   // Wait for a phase; false: it gave up, or another role did.
   auto wait = [&](uint64_t* bar, uint32_t parity) -> bool {
     if (mbar_try_wait(bar, parity)) return true;
-    return wait_long(bar, parity, &abort_flag, P.hdr);
+    return wait_long(bar, parity, &abort_flag, kWaitNs + kWaitRowNs * (uint64_t)P.max_rows, P.hdr);
   };
   // The same for a whole warp: one answer for all its lanes.
   auto warp_wait = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -930,8 +932,9 @@ void segments_of(GemmParams& P, const ExpertMatmul& a) {
   P.max_rows = a.assignments;
   P.E = a.E;
   P.capacity = a.capacity;
-  // ranking costs E^2 / 384 steps a CTA: where tiles are large enough to differ
-  P.sorted = a.E > 1 && a.assignments >= (int64_t)32 * a.E;
+  // ranking costs E^2 / 384 steps a CTA (4 us for 512 experts): where tiles are large
+  // enough to differ, and few enough experts
+  P.sorted = a.E > 1 && a.E <= 512 && a.assignments >= (int64_t)32 * a.E;
 }
 
 // The token operand's maps, and the tiles' shape.

@@ -199,6 +199,7 @@ __device__ __forceinline__ float key_bound(float v) { return 1.0e-6f + 2.5e-7f *
 // banks.
 struct GroupPlan {
   int G = 1, shift = 0, n = 1, start = 0;
+  uint32_t columns = 0u;  // G a multiple of 32: the columns of group 0, one bit each
   uint32_t magic = 0u;  // e / G == __umulhi(e, magic) for e < 2^16 (G > 1)
   __device__ void init(int E, int groups, int lane) {
     G = E / groups;
@@ -208,6 +209,7 @@ struct GroupPlan {
     const int unit = 1 << shift, g = lane >> shift, sub = lane & (unit - 1);
     start = sub + unit * g;
     if (start >= n) start = sub + unit * (g % ((n + unit - 1) >> shift));
+    columns = (G & 31) == 0 ? 0xffffffffu >> (32 - (G >> 5)) : 0u;
     magic = G > 1 ? (uint32_t)((0x100000000ull + (uint64_t)G - 1) / (uint64_t)G) : 0u;
   }
 };
@@ -310,26 +312,20 @@ __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k
     // of two scores (a group without a finite key scores -inf in any precision)
     // (maxima on order codes: the integer reduction is one instruction)
     const float big = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(mag)));
-    uint32_t kept = 0u, scode = order_code(score), best = 0u;
+    uint32_t kept = 0u, columns = 0u, scode = order_code(score), best = 0u;
     for (int r = 0; r < R.top_groups; ++r) {
       best = __reduce_max_sync(kFull, scode);
       const int who = __ffs(__ballot_sync(kFull, scode == best)) - 1;
       kept |= 1u << (who >> L.shift);
+      columns |= L.columns << ((who >> L.shift) * (G >> 5));
       if (lane == who) scode = 0u;
     }
     const uint32_t next = __reduce_max_sync(kFull, scode);
     // (code 0: no group is left, which does not happen below top_groups = groups)
     if (!(code_float(best) - code_float(next) > 4.0f * bound(big))) return false;
-    if ((G & 31) == 0) {
-      const int step = G >> 5;
-      int in = 0;
+    if ((G & 31) == 0) {  // whole columns: bit i says whether column i is kept
 #pragma unroll
-      for (int i = 0; i < NK; ++i) {
-        key[i] = (kept & 1u) ? key[i] : -INFINITY;
-        ++in;
-        kept >>= in == step ? 1 : 0;
-        in = in == step ? 0 : in;
-      }
+      for (int i = 0; i < NK; ++i) key[i] = (columns & (1u << i)) ? key[i] : -INFINITY;
     } else {
 #pragma unroll
       for (int i = 0; i < NK; ++i) {

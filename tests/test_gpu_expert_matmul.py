@@ -111,7 +111,8 @@ def test_activations_and_epilogue(name, bias, residual, pre):
     (1, 1, 1, 8, 8), (1, 4, 2, 64, 64), (2, 3, 1, 8, 264), (17, 2, 1, 72, 8), (15, 1, 1, 1000, 128),
     (16, 1, 1, 64, 128), (129, 1, 1, 64, 136), (255, 1, 1, 128, 256), (256, 1, 1, 128, 256),
     (257, 1, 1, 136, 248), (511, 2, 1, 520, 384), (1025, 3, 2, 256, 520), (600, 64, 6, 128, 72),
-    (40, 1024, 4, 64, 16), (4200, 1, 1, 64, 40),
+    (40, 1024, 4, 64, 16), (4200, 1, 1, 64, 40), (9000, 1024, 4, 16, 24), (2100, 512, 8, 24, 16),
+    (700, 5, 3, 64, 1032), (64, 1, 1, 4104, 64),
 ])
 @pytest.mark.parametrize("name", ["silu", "swiglu"])
 def test_sizes(T, E, k, K, F, name):
@@ -211,7 +212,7 @@ def test_gradients(name):
 @pytest.mark.parametrize("T,E,k,K,F", [
     (1, 1, 1, 8, 8), (1, 4, 2, 64, 64), (15, 1, 1, 264, 40), (16, 1, 1, 64, 128), (17, 2, 1, 72, 8),
     (64, 1, 1, 128, 128), (65, 1, 1, 520, 136), (300, 3, 2, 136, 264), (40, 128, 4, 64, 16),
-    (1100, 2, 1, 72, 264),
+    (1100, 2, 1, 72, 264), (3000, 1024, 4, 16, 24), (2100, 512, 8, 24, 16), (700, 5, 3, 648, 40),
 ])
 def test_gradient_sizes(T, E, k, K, F):
     _backward_case(T, E, k, K, F, "swiglu")
