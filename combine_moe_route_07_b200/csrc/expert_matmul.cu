@@ -216,7 +216,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     tma_prefetch_map(&P.mb[0]);
   }
   if (wid == 1) tmem_alloc(&tmem_slot, kTmemCols);
+  tc_fence_before();
   __syncthreads();
+  cluster_sync_all();  // the other CTA's barriers are ready too
+  tc_fence_after();
   pdl_wait();
   pdl_trigger();
   unsigned long long my_rows = 0ull;
@@ -287,10 +290,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       if (MODE != kWeights) first[at[i]] = (seg[i].rows + height - 1) / height;
     }
   }
-  tc_fence_before();
   __syncthreads();
-  cluster_sync_all();  // the other CTA's barriers are ready too
-  tc_fence_after();
   const uint32_t tmem = tmem_slot;
   int total;
   if constexpr (MODE == kWeights) {
