@@ -380,6 +380,37 @@ def test_bad_segments_are_reported_and_skipped():
     assert (g.grad_bias == 0).all()
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 elements in a matrix: the last rows are where they belong."""
+    m = _mod()
+    T, K, F, last = 70001, 8, 32768, 70001 - 130
+    assert T * F > 1 << 31
+    shape = m.MoeShape(tokens=T, hidden=8, experts=1, k=1, ranks=1)
+    ws = m.Workspace(shape)
+    x, w = torch.randn(T, K, device="cuda").to(torch.bfloat16), _weights(1, F, K, 2).cuda()
+    out = m.moe_expert_matmul(shape, x, w, ws=ws)
+    m.moe_check(ws)
+    for r in (slice(0, 64), slice(32768, 32800), slice(last, T)):
+        want, z, mag = ref.matmul(x[r].cpu(), w.cpu(), [slice(0, r.stop - r.start)])
+        _check(out[r], want, _sum_tol(K, mag) * (1 + U) + U * want.abs(),
+               torch.ones(r.stop - r.start, dtype=torch.bool), "out")
+    # rows and weights gradients over the same matrix
+    g = m.moe_expert_matmul_backward(shape, out, x, w, ws=ws, need_bias=True)
+    m.moe_check(ws)
+    d = out[last:].double().cpu()
+    gx = d @ w[0].double().cpu()
+    mx = d.abs() @ w[0].double().cpu().abs()
+    _check(g.grad_x[last:], gx, _sum_tol(F, mx) * (1 + U) + U * gx.abs(),
+           torch.ones(T - last, dtype=torch.bool), "grad_x")
+    cols = slice(F - 256, F)
+    dc = out[:, cols].double()
+    gw, mw = dc.T @ x.double(), dc.abs().T @ x.double().abs()
+    _check(g.grad_w[0, cols], gw.cpu(), (_sum_tol(T, mw) * (1 + U) + U * gw.abs()).cpu(),
+           torch.ones(256, dtype=torch.bool), "grad_w")
+    _check(g.grad_bias[:, cols], dc.sum(0)[None].cpu(), ((T + 16) * 2.0 ** -24 * dc.abs().sum(0))[None].cpu(),
+           torch.ones(1, dtype=torch.bool), "grad_bias")
+
+
 def test_wrong_tensors_are_refused():
     m = _mod()
     shape, ws, lay, segs, held = _layout(m, 10, 4, 1, seed=2)

@@ -253,6 +253,29 @@ def test_unaligned_rows_and_other_stream():
     assert torch.equal(grad[1:].view(T, E), whole) and grad[0] == 9.0
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 logits: the last tokens' rows are where they belong."""
+    m = _mod()
+    T, E, k = (1 << 21) + 37, 1024, 4
+    logits = torch.randn(1 << 14, E, device="cuda").repeat(T // (1 << 14) + 1, 1)[:T].contiguous()
+    logits[-64:] = _randn(64, E, seed=5).cuda()
+    shape = m.MoeShape(tokens=T, hidden=8, experts=E, k=k, ranks=1)
+    ws = m.Workspace(shape)
+    rule = m.ScoreRule("sigmoid", 8, 4, 2)
+    ids, gates = m.moe_route_scored(shape, logits, rule, ws=ws)
+    m.moe_check(ws)
+    want, g, _ = ref.route(logits[-64:].cpu(), k, "sigmoid", True, 8, 4, 2)
+    assert torch.equal(ids[-64:].cpu().long(), want)
+    assert ((gates[-64:].cpu().double() - g).abs() <= _gate_tol("sigmoid", True) * g).all()
+    grad = m.moe_route_scored_backward(shape, logits, rule, ids, gates, ws=ws)
+    m.moe_check(ws)
+    del logits
+    assert torch.isfinite(grad[-64:]).all()
+    off = torch.ones(64, E, dtype=torch.bool, device="cuda").scatter_(1, ids[-64:].long(), False)
+    assert (grad[-64:][off] == 0).all() and (grad[-64:][~off] != 0).any()
+    assert int((grad[: 1 << 14] != 0).sum()) <= (1 << 14) * k
+
+
 def test_no_tokens_and_wrong_arguments():
     m = _mod()
     shape = m.MoeShape(tokens=0, hidden=8, experts=8, k=2, ranks=1)
