@@ -43,8 +43,7 @@ constexpr int kABytes = kBM * kBK * 2;
 constexpr int kSlots = 8;     // slices in flight, at most (a power of two)
 constexpr int kEpiWarps = 8;
 constexpr int kGemmThreads = (4 + kEpiWarps) * 32;
-// Staging: two 32 x 32 bf16 blocks a warp; weights gradient one of 32 x 128.
-constexpr int epi_bytes(bool weights) { return kEpiWarps * (weights ? 8192 : 4096); }
+constexpr int kEpiBytes = kEpiWarps * 4096;  // two 32 x 32 bf16 blocks a warp, or one 32 x 64
 constexpr int kMaxSlice = kABytes + 128 * kBK * 2;
 constexpr int kTmemCols = 512;
 // The longest wait: two seconds, and 20 ns for each row (the weights gradient of one
@@ -73,7 +72,7 @@ struct GemmParams {
   int cols;    // weights gradient: columns of x
   int band;    // token tiles an expert walks together
   int adapt;   // choose the tiles' height by the rounds they take
-  int ring;    // bytes of the operand ring
+  int smem;    // bytes of dynamic shared memory
   int sorted;  // experts in descending order of their rows (see my_tile)
   int act;
 };
@@ -182,15 +181,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
   __shared__ unsigned long long rows_sum;
   __shared__ int tiles_at[kHeights];
   __shared__ int32_t warp_tot[kGemmThreads / 32];
-  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
-                                             ~uintptr_t(1023));
-  uint8_t* epi = smem + P.ring;
-  int32_t* seg_off = reinterpret_cast<int32_t*>(epi + epi_bytes(MODE == kWeights));
+  // The segment table: offsets, rows, exclusive prefix of token tiles [E+1] (forward /
+  // rows), and the experts in the table's order.  Behind it, from a 1024-byte boundary
+  // on, the operand ring in whole KiB, and the staging blocks.
+  int32_t* seg_off = reinterpret_cast<int32_t*>(smem_raw);
   int32_t* seg_rows = seg_off + P.E;
-  // exclusive prefix of token tiles [E+1] (forward / rows), and the experts in the
-  // table's order [E]
   int32_t* first = seg_rows + P.E;
   int32_t* expert = first + P.E + 1;
+  uint8_t* smem = reinterpret_cast<uint8_t*>(
+      (reinterpret_cast<uintptr_t>(expert + P.E) + 1023) & ~uintptr_t(1023));
+  const int ring = (int)(smem_raw + P.smem - smem - kEpiBytes) & ~1023;
+  uint8_t* epi = smem + ring;
 
   const int tid = threadIdx.x, lane = tid & 31, wid = tid >> 5;
   const uint32_t rank = cluster_rank();
@@ -382,7 +383,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
                                        : box_rows(r.n / 2) * (kBK * 2));
   };
   auto place = [&](int& head, int bytes) -> int {
-    if (head + bytes > P.ring) head = 0;
+    if (head + bytes > ring) head = 0;
     const int at = head;
     head += bytes;
     return at;
@@ -411,7 +412,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     // ---- producers: warp 0 the M operand, warp 2 the N operand --------------------
     if (elect_one()) {
       uint32_t it = 0, old = 0;  // slices issued, and those known to be used up
-      int head = 0, room = P.ring;
+      int head = 0, room = ring;
       int* const mine = taken[wid >> 1];
       const uint32_t even_full = even_addr(&full[0]), own_landed = smem_addr(&landed[0]);
       bool ok = true;
@@ -429,8 +430,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
         for (int k0 = 0; k0 < depth; k0 += kBK, ++it) {
           const uint32_t s = it % kSlots;
           int need = bytes;
-          if (head + bytes > P.ring) {  // (as place())
-            need += P.ring - head;
+          if (head + bytes > ring) {  // (as place())
+            need += ring - head;
             head = 0;
           }
           // the oldest slices make room: for the bytes, and for the slot
@@ -658,10 +659,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
       const int nchunks = (rows + 31) >> 5;
       if constexpr (MODE == kWeights) {
         // Warps 4..7 take columns 0..127, warps 8..11 the others, 64 at a time.  A lane
-        // holds 32 columns of one row of dW; 32 rows of 128 bytes (16-byte pieces
-        // swizzled by the row) are staged in one of two 4 KiB blocks and stored as one
-        // box while the other block is filled.  (Boxes of 32 x 32 held the gradient of
-        // 256-row experts at 3.2 TB/s, one block of 8 KiB at 3.7.)
+        // holds 32 columns of one row of dW; 32 rows of 128 bytes (16-byte pieces swizzled
+        // by the row) are staged and stored as one box.  (Boxes of 32 x 32 held the
+        // gradient of 256-row experts at 3.2 TB/s; a second staging block per warp, which
+        // costs a stage of the ring, at 3.9 instead of 4.1.)
         const int col0 = half * 128, ncols = min(128, rows - col0);
         uint32_t v[32];
 #pragma unroll
@@ -670,9 +671,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           if (j * 32 < ncols) {
-            uint8_t* buf = epi + (wid - 4) * 8192 + (j >> 1) * 4096;
+            uint8_t* buf = epi + (wid - 4) * 4096;
             if ((j & 1) == 0) {
-              if (elect_one()) bulk_wait_read<1>();
+              if (elect_one()) bulk_wait_read<0>();
               __syncwarp();
             }
             uint32_t w[16];
@@ -695,8 +696,6 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
             }
           }
         }
-        // (both blocks take turns: a tile that ends after the first gives the second's turn)
-        if (ncols <= 64 && elect_one()) bulk_commit();
       } else {
         const int64_t row = (int64_t)seg_off[r.seg] + row0;
         const bool up_half = GATED && q >= 2;
@@ -895,8 +894,7 @@ int64_t max_token_tiles(int64_t assignments, int E, int64_t bn) {
   return assignments / bn + (assignments < E ? assignments : E);
 }
 
-constexpr size_t kSmemLimit = 227 * 1024;
-constexpr size_t kSmemStatic = 1024;  // bounds the kernel's static shared memory
+constexpr int kSmemLimit = 227 * 1024;  // of a CTA, static and dynamic
 
 template <int MODE, bool GATED>
 cudaError_t launch_gemm(const LaunchEnv& env, GemmParams& P, int64_t max_tiles = 0) {
@@ -909,14 +907,21 @@ cudaError_t launch_gemm(const LaunchEnv& env, GemmParams& P, int64_t max_tiles =
     P.adapt = max_tiles <= 16 * all;
     if (P.adapt) max_tiles = max_token_tiles(P.max_rows, P.E, 32) * ct;
   }
-  const size_t table = sizeof(int32_t) * ((size_t)P.E * 4 + 1);
-  const size_t smem = kSmemLimit - kSmemStatic;
-  P.ring = (int)((smem - 1024 - epi_bytes(MODE == kWeights) - table) / 1024 * 1024);
-  static_assert(kSmemLimit - kSmemStatic - 1024 - epi_bytes(false) - 17 * 1024 >= 5 * kMaxSlice &&
-                    kSmemLimit - kSmemStatic - 1024 - epi_bytes(true) - 17 * 1024 >= 4 * kMaxSlice,
-                "five of the largest slices, four of the weights gradient's");
-  int per_sm = 1;
   const auto kernel = expert_gemm_kernel<MODE, GATED>;
+  static const int static_bytes = [&] {
+    cudaFuncAttributes attr = {};
+    return cudaFuncGetAttributes(&attr, (const void*)kernel) == cudaSuccess
+               ? (int)attr.sharedSizeBytes
+               : -1;
+  }();
+  if (static_bytes < 0) return cudaErrorInvalidDeviceFunction;
+  // room for the table, the boundary behind it, the staging blocks and five of the
+  // largest slices at E = 1024 (six up to E of about 160)
+  static_assert(kSmemLimit - 1024 - (16 * 1024 + 4) - 1023 - kEpiBytes >= 5 * kMaxSlice, "five slices");
+  const size_t smem = (size_t)(kSmemLimit - static_bytes);
+  if (static_bytes > 1024) return cudaErrorInvalidConfiguration;
+  P.smem = (int)smem;
+  int per_sm = 1;
   cudaError_t err = blocks_per_sm((const void*)kernel, kGemmThreads, smem, &per_sm);
   if (err != cudaSuccess) return err;
   int64_t pairs = max_tiles < all ? max_tiles : all;
