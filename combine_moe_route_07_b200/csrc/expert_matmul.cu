@@ -16,14 +16,28 @@
 // weights, and a row of another expert that a tile's copy brings along can
 // never reach this expert's sums (columns of D are independent).
 //
-// Persistent pairs of CTAs (cta_group::2), one CTA per SM: in each CTA a
-// producer thread feeds a ring of 6 stages of 32 KiB by tensor-map copies
-// (64-deep slices, 128-byte swizzle), the even CTA's issuing thread runs the
-// matrix instructions of both, and eight warps of each drain the accumulator
-// of the previous tile meanwhile (two accumulators in tensor memory).  A pair
-// shares its operands, so a 256 x 256 tile costs each SM 32 KiB of copies per
-// 64-deep slice; one CTA alone moves 48 KiB for the same work and is bound by
-// the L2 (about 10 TB/s).  Every wait is bounded.
+// Persistent pairs of CTAs (cta_group::2), one CTA per SM: in each CTA two producer
+// threads (one an operand) feed a ring of shared memory by tensor-map copies (64-deep
+// slices, 128-byte swizzle; a slice takes the bytes its tile's rows need, so the ring
+// holds six full slices of 32 KiB or eight narrow ones), one thread of the even CTA
+// issues the matrix instructions of both, and eight warps of each drain the
+// accumulator of the previous tile meanwhile (two accumulators in tensor memory).  A
+// pair shares its operands: a 256 x 256 tile costs each SM 32 KiB of copies per
+// slice, where one CTA alone would move 48 KiB for the same work.  With swiglu a
+// tile is 128 channels: gates in lanes 0..63 of each CTA's accumulator, the same
+// channels' ups in lanes 64..127.  Every wait is bounded.
+//
+// What decides, by size (one B200, short runs at 1.9 GHz; long ones are held to the
+// board's 1000 W, down to 1.2 GHz, and take a fifth longer):
+//   18944 rows, 4096 x 2048, one expert: 208 us, 1530 TFLOP/s; tensor pipe 90 % active
+//   64 experts x 4 rows, 4096 x 2048: 172 us, 6.25 TB/s: the weights' stream
+//   64 experts x 256 rows: 243 us, 1130 TFLOP/s and 5.2 TB/s: both
+//   its weights gradient: 305 us, 900 TFLOP/s, 1.07 GB written at 3.5 TB/s (a plain
+//     fill of as much takes 270 us)
+// Most of the way there was the length of the issuing threads' loops: behind a test
+// of the lane number every copy and matrix instruction sits in a loop over the lanes
+// (about 100 ns each; elect.sync removes it), and one producer thread for both
+// operands took 900 cycles a slice.
 #include <limits.h>
 #include <math.h>
 
