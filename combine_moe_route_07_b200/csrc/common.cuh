@@ -86,6 +86,23 @@ __device__ __forceinline__ void st16(void* p, const uint4& v) {
   *reinterpret_cast<uint4*>(p) = v;
 }
 
+// 2^x within 2 units in the last place and 1/x within 1, subnormals flushed; the
+// logistic function from them (within 2^-21 of itself for |x| < 8, 2^-18 for |x| < 64:
+// the rounding of x log2(e) grows with x).  The library's fast forms handle subnormals
+// too, at about three times the instructions.
+__device__ __forceinline__ float ex2_f(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float rcp_f(float x) {
+  float r;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+constexpr float kLog2e = 1.44269504f;
+__device__ __forceinline__ float sigmoid_f(float x) { return rcp_f(1.0f + ex2_f(x * -kLog2e)); }
+
 // bf16 pair <-> fp32 (exact widening; nearest-even narrowing).
 __device__ __forceinline__ float bf16lo(uint32_t w) { return __uint_as_float(w << 16); }
 __device__ __forceinline__ float bf16hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }

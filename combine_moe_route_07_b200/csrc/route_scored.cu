@@ -174,19 +174,6 @@ __device__ __noinline__ bool scored_token_slow(const float* row, const float* bi
   return scored_token_exact(row, bias, E, k, R, lane, key, sel_e, sel_s);
 }
 
-// 2^x within 2 units in the last place and 1/x within 1 (flushing subnormals).
-__device__ __forceinline__ float ex2_f(float x) {
-  float r;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-__device__ __forceinline__ float rcp_f(float x) {
-  float r;
-  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-  return r;
-}
-constexpr float kLog2e = 1.44269504f;
-
 // How far a binary32 key can be from its binary64 value: a score is within 2^-21
 // (2^x is off by 2^-22, its argument's rounding is damped by the score, the
 // reciprocal and the softmax's sum add 2^-23 each), one addition adds 2^-24 of the
@@ -253,7 +240,7 @@ __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k
       v = ex2_f((l - m) * kLog2e);
       return BIAS ? fmaf(v, scale, __ldg(bias + e)) : v;
     }
-    v = rcp_f(1.0f + ex2_f(l * -kLog2e));
+    v = sigmoid_f(l);
     return BIAS ? v + __ldg(bias + e) : v;
   };
   if (!SOFTMAX || !raw) {
