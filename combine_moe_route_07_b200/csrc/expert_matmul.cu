@@ -178,8 +178,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kGemmThreads, 1)
     expert_gemm_kernel(const __grid_constant__ GemmParams P) {
   constexpr int kTileM = GATED ? kBM : 2 * kBM;  // output channels of a pair's tile
   extern __shared__ uint8_t smem_raw[];
-  // full, tempty and fixed are waited on by the even CTA only.  A slot's barriers see at most one phase at a
-  // time: the slot is used again only once the instructions that read it are done.
+  // full, tempty and fixed are waited on by the even CTA only.  A slot's barriers see at
+  // most one phase at a time: the slot is used again only once the instructions that
+  // read it are done.
   __shared__ uint64_t full[kSlots], empty[kSlots], tfull[2], tempty[2], drain;
   // weights gradient, slices with stale rows: this CTA's half has landed; both
   // CTAs' stale rows are zero

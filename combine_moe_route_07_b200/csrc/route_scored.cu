@@ -174,10 +174,13 @@ __device__ __noinline__ bool scored_token_slow(const float* row, const float* bi
   return scored_token_exact(row, bias, E, k, R, lane, key, sel_e, sel_s);
 }
 
-// How far a binary32 key can be from its binary64 value: a score is within 2^-21
-// (2^x is off by 2^-22, its argument's rounding is damped by the score, the
-// reciprocal and the softmax's sum add 2^-23 each), one addition adds 2^-24 of the
-// key.
+// How far a binary32 key can be from its binary64 value.  A score of its own is within
+// 2^-21 (2^x is off by 2^-22, its argument's rounding is damped by the score, the
+// reciprocal adds 2^-23), one addition adds 2^-24 of the key.  The softmax's sum is
+// off by at most 1.5e-6 of itself (14 additions, 2^x and its arguments, the reciprocal),
+// alike for every score of the token: two keys move apart by that times the difference
+// of their scores, which is at most 1, and by 2^-22 of the scores' sum: less than the
+// 2e-6 by which two bounds keep keys apart.
 __device__ __forceinline__ float key_bound(float v) { return 1.0e-6f + 2.5e-7f * fabsf(v); }
 
 // What the group scoring needs of the sizes, computed once: unit = 1 << shift lanes a
@@ -207,8 +210,8 @@ template <int NK, bool SOFTMAX, bool BIAS, bool GROUPED, bool FULL>
 __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k,
                                                   const ScoreRule& R, const GroupPlan& L, int lane,
                                                   uint32_t vmask, const float* __restrict__ bias,
-                                                  float* skey,
-                                                  CandArea* C, int& sel_e, double& sel_s) {
+                                                  float* skey, CandArea* C, int& sel_e,
+                                                  double& sel_s) {
   // without a bias the logits are in the softmax's order (but their sums are not)
   const bool raw = SOFTMAX && !BIAS && !(GROUPED && R.group_top == 2);
   auto valid = [&](int i) { return FULL || ((vmask >> i) & 1u) != 0u; };
@@ -224,9 +227,11 @@ __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k
     m = code_float(__reduce_max_sync(kFull, order_code(m)));
     if (!(fabsf(m) < INFINITY)) return false;  // a row without a finite maximum
     if (BIAS || !R.renorm) {
-      float part = 0.0f;
+      // four partial sums: at most 14 roundings of 2^-24 with the shuffles
+      float p4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-      for (int i = 0; i < NK; ++i) part += ex2_f((key[i] - m) * kLog2e);
+      for (int i = 0; i < NK; ++i) p4[i & 3] += ex2_f((key[i] - m) * kLog2e);
+      float part = (p4[0] + p4[1]) + (p4[2] + p4[3]);
 #pragma unroll
       for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kFull, part, o);
       scale = __fdividef(1.0f, part);
@@ -465,8 +470,8 @@ __global__ void __launch_bounds__(kScoredWarps * 32, scored_min_blocks(NK))
     __syncwarp();
     int e = 0;
     double s = 0.0;
-    bool ok = fast && scored_token_fast<NK, SOFTMAX, BIAS, GROUPED, FULL>(rows + turn * stride, E, k, R, plan, lane,
-                                                                vmask, bias, skey, C, e, s);
+    bool ok = fast && scored_token_fast<NK, SOFTMAX, BIAS, GROUPED, FULL>(
+                          rows + turn * stride, E, k, R, plan, lane, vmask, bias, skey, C, e, s);
     if (!ok) {
       // the exact form's keys take both staged rows: the next one is staged again
       asm volatile("cp.async.wait_group 0;" ::: "memory");
@@ -495,8 +500,8 @@ __global__ void __launch_bounds__(kScoredWarps * 32, scored_min_blocks(NK))
 constexpr int kBackWarps = 8;
 
 // The sum, or largest value, over the W lanes of a token.
-template <int W>
-__device__ __forceinline__ float lanes_sum(float v) {
+template <int W, typename F>
+__device__ __forceinline__ F lanes_sum(F v) {
 #pragma unroll
   for (int o = W / 2; o > 0; o >>= 1) v += __shfl_xor_sync(kFull, v, o);
   return v;
@@ -564,21 +569,32 @@ __global__ void __launch_bounds__(kBackWarps * 32)
     up = e >= 0 ? (float)((double)up * R.scale) : 0.0f;
     float d;
     if (R.softmax) {  // renormalised: the softmax of the chosen
+      // (a bias can choose masked experts alone: gates of zero, no gradient)
       const float m = lanes_max<W>(e >= 0 ? l : -INFINITY);
-      const float x = e >= 0 ? expf(l - m) : 0.0f;
-      const float p = x * (1.0f / lanes_sum<W>(x));
+      const float x = e >= 0 && l != -INFINITY ? expf(l - m) : 0.0f;
+      const float sum = lanes_sum<W>(x);
+      const float p = sum != 0.0f ? x * (1.0f / sum) : 0.0f;
       d = p * (up - lanes_sum<W>(up * p));
     } else {
       // sigmoid(l) and 1 - sigmoid(l), both without cancellation
       const float x = expf(-fabsf(l));
       const float big = 1.0f / (1.0f + x), small = x * big;
       const float s = e >= 0 ? (l >= 0.0f ? big : small) : 0.0f, c = l >= 0.0f ? small : big;
-      d = up;
+      d = up * s;
       if (R.renorm) {
         const float sum = lanes_sum<W>(s), us = lanes_sum<W>(up * s);
-        d = sum > 0.0f ? (up - us / sum) / sum : 0.0f;
+        d = sum > 0.0f ? s / sum * (up - us / sum) : 0.0f;
+        // scores near or below binary32's range: their quotients in binary64, as the gates'
+        const bool tiny = sum < 0x1p-100f;
+        if (__any_sync(kFull, tiny && e >= 0)) {
+          const double sd = e >= 0 ? 1.0 / (1.0 + exp(-(double)l)) : 0.0;
+          const double sumd = lanes_sum<W>(sd);
+          const float q = sumd > 0.0 ? (float)(sd / sumd) : 0.0f;
+          const float uq = lanes_sum<W>(up * q);
+          if (tiny) d = q * (up - uq);
+        }
       }
-      d = e >= 0 ? d * s * c : 0.0f;
+      d = e >= 0 ? d * c : 0.0f;
     }
     d = merge_slots<W>(d, e, lane);
     __syncwarp();

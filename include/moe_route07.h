@@ -419,9 +419,9 @@ moe_status_t moe_expert_matmul_backward(const moe_shape_t* shape, int32_t in_fea
  *   grad_y[dst_pos[t,j],:] = bf16(gates[t,j] * grad_out[t,:])   bf16 [N,H]
  *   grad_gates[t,j]        = <grad_out[t,:], y[dst_pos[t,j],:]> fp32 [T,k]
  * A dropped slot (dst_pos < 0) gets grad_gates of 0; rows no slot maps to are
- * not written; no two slots may share a row (a layout's never do).  A dst_pos value >= N sets MOE_ERR_DEVICE_RANGE and counts as
- * dropped.  Sums are fp32 in a fixed order.  Buffers and alignment as
- * moe_combine. */
+ * not written; no two slots may share a row (a layout's never do).  A dst_pos
+ * value >= N sets MOE_ERR_DEVICE_RANGE and counts as dropped.  Sums are fp32 in
+ * a fixed order.  Buffers and alignment as moe_combine. */
 moe_status_t moe_combine_backward(const moe_shape_t* shape, const void* grad_out, const void* y,
                                   const int32_t* dst_pos, const float* gates, void* grad_y,
                                   float* grad_gates, void* ws, size_t ws_bytes,

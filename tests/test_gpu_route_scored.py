@@ -231,6 +231,49 @@ def test_gradient_edges():
         assert (got.abs() <= 2.0 ** -100).all()
 
 
+def test_gradient_of_scores_below_fp32():
+    """Sigmoid scores whose chosen sum is near or below fp32's smallest number: the gates are quotients
+    of them all the same, and so are the gradients."""
+    m = _mod()
+    T, E, k = 96, 64, 5
+    top = torch.linspace(-60.0, -600.0, T)[:, None]
+    logits = top + _randn(T, E, seed=4)
+    up = _randn(T, k, seed=5)
+    logits[7] = -800.0  # scores that binary64 loses too: gates and gradients of zero
+    ids, gates, _ = _run(logits, k, "sigmoid", True)
+    _compare(logits, k, "sigmoid", True)
+    assert (gates[7] == 0).all()
+    shape = m.MoeShape(tokens=T, hidden=8, experts=E, k=k, ranks=1, renorm=True)
+    got = m.moe_route_scored_backward(shape, logits.cuda(), m.ScoreRule("sigmoid"), ids.int().cuda(),
+                                      up.cuda(), ws=m.Workspace(shape)).cpu().double()
+    at = ids.cpu().long()
+    s = ref.scores(torch.gather(logits, 1, at), "sigmoid")
+    total = s.sum(1, keepdim=True)
+    q = torch.where(total > 0, s / total, torch.zeros_like(s))
+    part = q * (up.double() - (q * up.double()).sum(1, keepdim=True)) * (1.0 - s)
+    want = torch.zeros(T, E, dtype=torch.float64).scatter_add_(1, at, part)
+    # quotients within 2^-21 (exp and the division in fp32), their weighted sum of k parts likewise
+    assert ((got - want).abs() <= 2.0 ** -19 * up.double().abs().sum(1, keepdim=True)).all()
+    assert (got[7] == 0).all() and (got[T - 1] != 0).any()
+
+
+def test_a_bias_that_chooses_masked_experts():
+    """Softmax over masked logits: a bias can choose experts of score zero alone."""
+    m = _mod()
+    T, E, k = 6, 48, 4
+    for W in (k, 20):  # both sizes of a token's lane group
+        logits = _randn(T, E, seed=1)
+        logits[:, :W] = -float("inf")
+        bias = torch.zeros(E)
+        bias[:W] = 3.0 - 0.01 * torch.arange(W)
+        ids, gates, _ = _run(logits, W, "softmax", True, bias=bias)
+        assert (gates == 0).all() and torch.equal(ids.cpu().long(), torch.arange(W).expand(T, W))
+        shape = m.MoeShape(tokens=T, hidden=8, experts=E, k=W, ranks=1, renorm=True)
+        got = m.moe_route_scored_backward(shape, logits.cuda(), m.ScoreRule("softmax"), ids.int().cuda(),
+                                          _randn(T, W, seed=2).cuda(), ws=m.Workspace(shape))
+        assert (got == 0).all()
+
+
 def test_unaligned_rows_and_other_stream():
     """Logits and outputs that start 4 bytes behind a 16-byte boundary, on a stream of their own."""
     m = _mod()
