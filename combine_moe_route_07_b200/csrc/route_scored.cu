@@ -16,15 +16,15 @@
 // keys of a token are formed in binary32 with a bound on their error, and
 // binary64 decides among the few that the bound leaves open:
 //   1. group scores in binary32; the kept groups are certain when the gap
-//      between the last kept and the first left out exceeds the bound;
+//      between the last kept and the first left out exceeds the bound, else the
+//      keys that count in them are taken in binary64;
 //   2. tau = the k-th largest lane maximum of the kept keys, less the bound: no
 //      key below it can be among the k best; the keys at or above it (k to k+4
 //      of them, usually) are compacted, one a lane;
 //   3. they are ranked by their binary32 keys; where two neighbours among the k
 //      best are closer than the bound, by their binary64 keys, ties by expert.
-// A token whose groups or candidates stay open (ties, masks that leave less
-// than k finite keys, NaN, more than 32 candidates) is decided in binary64
-// throughout, out of line.
+// A token whose candidates stay open (masks that leave less than k finite keys,
+// NaN, more than 32 candidates) is decided in binary64 throughout, out of line.
 #include <math.h>
 
 #include "common.cuh"
@@ -186,23 +186,66 @@ __device__ __forceinline__ float key_bound(float v) { return 1.0e-6f + 2.5e-7f *
 // What the group scoring needs of the sizes, computed once: unit = 1 << shift lanes a
 // group (a power of two) walk its n pieces (16 bytes, or single keys where groups are
 // not whole pieces) from `start` on, in turns that keep the groups' lanes on different
-// banks.
+// banks.  even: every lane has as many whole pieces (the groups a power of two, and
+// all E experts there).
 struct GroupPlan {
   int G = 1, shift = 0, n = 1, start = 0;
-  uint32_t columns = 0u;  // G a multiple of 32: the columns of group 0, one bit each
+  bool even = false;
+  // of this lane's group (0: none), one bit each: its columns of 32 experts where groups
+  // are whole columns, else the group itself
+  uint32_t bits = 0u;
   uint32_t magic = 0u;  // e / G == __umulhi(e, magic) for e < 2^16 (G > 1)
   __device__ void init(int E, int groups, int lane) {
     G = E / groups;
     if (groups > 32) return;  // (the exact form's)
     shift = 31 - __clz(32 / groups);
     n = (G & 3) == 0 ? G >> 2 : G;
+    even = (groups & (groups - 1)) == 0 && (G & 3) == 0 && (E & 127) == 0;
     const int unit = 1 << shift, g = lane >> shift, sub = lane & (unit - 1);
     start = sub + unit * g;
     if (start >= n) start = sub + unit * (g % ((n + unit - 1) >> shift));
-    columns = (G & 31) == 0 ? 0xffffffffu >> (32 - (G >> 5)) : 0u;
+    if (g < groups) bits = (G & 31) == 0 ? (kFull >> (32 - (G >> 5))) << (g * (G >> 5)) : 1u << g;
     magic = G > 1 ? (uint32_t)((0x100000000ull + (uint64_t)G - 1) / (uint64_t)G) : 0u;
   }
 };
+
+// 1 / sum of the row's exponentials, summed as the exact form sums them.
+__device__ __noinline__ double softmax_scale_d(const float* row, int E, double m, int lane) {
+  double s = 0.0;
+  for (int e = lane; e < E; e += 32) s += exp((double)row[e] - m);
+  return 1.0 / wsum_d(s);
+}
+
+// The kept groups' bits by binary64 scores, where binary32 leaves them open:
+// keys below `low` are not among the ones that count in this lane's group.  (Decided by
+// the exact form, one such token held its warp for 15 us at the end of a 70 us kernel.)
+__device__ __noinline__ uint32_t open_groups(const float* row, const float* __restrict__ bias,
+                                             const float* skey, const ScoreRule& R, int G,
+                                             int shift, uint32_t bits, float low, double m,
+                                             double inv_sum, int lane) {
+  const int unit = 1 << shift, g = lane >> shift, sub = lane & (unit - 1);
+  double a = -INFINITY, b = -INFINITY;
+  if (g < R.groups)
+    for (int e = g * G + sub; e < (g + 1) * G; e += unit)
+      if (skey[e] >= low) {
+        double v = score_d((double)row[e], m, inv_sum, R.softmax != 0);
+        if (bias != nullptr) v += (double)__ldg(bias + e);
+        b = fmax(b, fmin(a, v));
+        a = fmax(a, v);
+      }
+  for (int o = 1; o < unit; o <<= 1) {
+    const double oa = __shfl_xor_sync(kFull, a, o), ob = __shfl_xor_sync(kFull, b, o);
+    b = fmax(fmin(a, oa), fmax(b, ob));
+    a = fmax(a, oa);
+  }
+  const double score = R.group_top == 2 ? a + b : a;
+  int rank = 0;
+  for (int j = 0; j < R.groups; ++j) {
+    const double other = __shfl_sync(kFull, score, j << shift);
+    rank += (other > score || (other == score && j < g)) ? 1 : 0;
+  }
+  return __reduce_or_sync(kFull, rank < R.top_groups ? bits : 0u);
+}
 
 // One token, decided as described above; false: not decided.  Lane j < k returns
 // slot j's expert and score.  `row` is the staged row.
@@ -263,12 +306,25 @@ __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k
     for (int i = 0; i < NK; ++i)
       if (valid(i)) skey[lane + 32 * i] = key[i];
     __syncwarp();
-    float a = -INFINITY, b = -INFINITY;
+    float a = -INFINITY, b = -INFINITY;  // the group's two largest keys (NaN: in a)
     auto take = [&](float v) {
       b = fmaxf(b, fminf(a, v));
       a = max2_nan(a, v);
     };
-    if (g < R.groups) {
+    if (FULL && NK >= 4 && L.even) {
+      // (each step straight-line: the general walk below cost 24 of 96 us at 65536 x 512)
+      constexpr int kSteps = NK >= 4 ? NK / 4 : 1;
+      const float4* part = reinterpret_cast<const float4*>(skey + g * G) + sub;
+#pragma unroll
+      for (int it = 0; it < kSteps; ++it) {
+        const float4 q = part[((g ^ it) & (kSteps - 1)) << L.shift];
+        const float h0 = max2_nan(q.x, q.y), l0 = fminf(q.x, q.y);
+        const float h1 = max2_nan(q.z, q.w), l1 = fminf(q.z, q.w);
+        const float h = max2_nan(h0, h1), l = max3_nan(fminf(h0, h1), l0, l1);
+        b = max3_nan(b, l, fminf(a, h));
+        a = max2_nan(a, h);
+      }
+    } else if (g < R.groups) {
       const float* part = skey + g * G;
       const int n = L.n;
       int at = L.start;
@@ -295,29 +351,50 @@ __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k
       b = fmaxf(fminf(a, oa), fmaxf(b, ob));
       a = fmaxf(a, oa);
     }
-    float score = -INFINITY, mag = 0.0f;  // lane `unit * g`: group g
-    if (g < R.groups && sub == 0) {
-      score = R.group_top == 2 ? a + b : a;
-      if (score > -INFINITY) mag = fmaxf(fabsf(a), R.group_top == 2 ? fabsf(b) : 0.0f);
-    }
+    const float score = g < R.groups ? (R.group_top == 2 ? a + b : a) : -INFINITY;
+    float mag = 0.0f;
+    if (score > -INFINITY) mag = fmaxf(fabsf(a), R.group_top == 2 ? fabsf(b) : 0.0f);
     // the kept groups, certain if the best one left out is further off than the errors
-    // of two scores (a group without a finite key scores -inf in any precision)
+    // of two scores (a group without a finite key scores -inf in any precision), else
+    // decided by their binary64 scores
     // (maxima on order codes: the integer reduction is one instruction)
     const float big = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(mag)));
-    uint32_t kept = 0u, columns = 0u, scode = order_code(score), best = 0u;
-    for (int r = 0; r < R.top_groups; ++r) {
-      best = __reduce_max_sync(kFull, scode);
-      const int who = __ffs(__ballot_sync(kFull, scode == best)) - 1;
-      kept |= 1u << (who >> L.shift);
-      columns |= L.columns << ((who >> L.shift) * (G >> 5));
-      if (lane == who) scode = 0u;
+    uint32_t kept = 0u, best, next;
+    if (R.groups <= 8) {
+      // a group's rank: each of its lanes compares it with every unit-th group
+      const uint32_t scode = order_code(score), mine = unit == 32 ? kFull : (1u << unit) - 1u;
+      int rank = 0;
+      for (int j = sub; j < R.groups + sub; j += unit) {
+        const uint32_t other = __shfl_sync(kFull, scode, j << L.shift);
+        const uint32_t above = __ballot_sync(kFull, j < R.groups && other > scode);
+        rank += __popc((above >> (g << L.shift)) & mine);
+      }
+      const bool keep = g < R.groups && rank < R.top_groups;
+      best = __reduce_min_sync(kFull, keep ? scode : 0xffffffffu);
+      next = __reduce_max_sync(kFull, keep || g >= R.groups ? 0u : scode);
+      kept = __reduce_or_sync(kFull, keep ? L.bits : 0u);
+      // (equal scores across the boundary keep more)
+      if (__popc(__ballot_sync(kFull, keep)) != R.top_groups << L.shift) next = best;
+    } else {
+      uint32_t scode = sub == 0 && g < R.groups ? order_code(score) : 0u;
+      best = 0u;
+      for (int r = 0; r < R.top_groups; ++r) {
+        best = __reduce_max_sync(kFull, scode);
+        const int who = __ffs(__ballot_sync(kFull, scode == best)) - 1;
+        kept |= __shfl_sync(kFull, L.bits, who);
+        if (lane == who) scode = 0u;
+      }
+      next = __reduce_max_sync(kFull, scode);
     }
-    const uint32_t next = __reduce_max_sync(kFull, scode);
-    // (code 0: no group is left, which does not happen below top_groups = groups)
-    if (!(code_float(best) - code_float(next) > 4.0f * bound(big))) return false;
+    if (!(code_float(best) - code_float(next) > 4.0f * bound(big))) {
+      const float last = R.group_top == 2 ? b : a;
+      const double md = (double)m;
+      kept = open_groups(row, BIAS ? bias : nullptr, skey, R, G, L.shift, L.bits,
+                         last - 2.0f * bound(big), md, SOFTMAX ? softmax_scale_d(row, E, md, lane) : 1.0, lane);
+    }
     if ((G & 31) == 0) {  // whole columns: bit i says whether column i is kept
 #pragma unroll
-      for (int i = 0; i < NK; ++i) key[i] = (columns & (1u << i)) ? key[i] : -INFINITY;
+      for (int i = 0; i < NK; ++i) key[i] = (kept & (1u << i)) ? key[i] : -INFINITY;
     } else {
 #pragma unroll
       for (int i = 0; i < NK; ++i) {
@@ -381,10 +458,10 @@ __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k
   }
   if (lane < total) C->slot[n] = lane;
   if (__any_sync(kFull, lane < total && n < k && within - n != 1)) {
-    if (SOFTMAX && BIAS) return false;  // (needs the binary64 sum too)
+    const double inv = SOFTMAX && BIAS ? softmax_scale_d(row, E, (double)m, lane) : 1.0;
     double d = 0.0;
     if (lane < total) {
-      d = score_d((double)row[e], (double)m, 1.0, SOFTMAX);
+      d = score_d((double)row[e], (double)m, inv, SOFTMAX);
       if (BIAS) d += (double)__ldg(bias + e);
       C->key[lane] = d;
     }
