@@ -37,6 +37,10 @@ namespace {
 
 constexpr int kScoredWarps = 4;
 
+// Groups of experts: none, any, or a power of two of them whose keys are as many whole
+// 16-byte pieces for every lane (E = 32 NK, E / groups a multiple of 4).
+enum { kNoGroups = 0, kAnyGroups = 1, kEvenGroups = 2 };
+
 __device__ __forceinline__ double wmax_d(double v) {
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) v = fmax(v, __shfl_xor_sync(kFull, v, o));
@@ -186,11 +190,9 @@ __device__ __forceinline__ float key_bound(float v) { return 1.0e-6f + 2.5e-7f *
 // What the group scoring needs of the sizes, computed once: unit = 1 << shift lanes a
 // group (a power of two) walk its n pieces (16 bytes, or single keys where groups are
 // not whole pieces) from `start` on, in turns that keep the groups' lanes on different
-// banks.  even: every lane has as many whole pieces (the groups a power of two, and
-// all E experts there).
+// banks.
 struct GroupPlan {
   int G = 1, shift = 0, n = 1, start = 0;
-  bool even = false;
   // of this lane's group (0: none), one bit each: its columns of 32 experts where groups
   // are whole columns, else the group itself
   uint32_t bits = 0u;
@@ -200,7 +202,6 @@ struct GroupPlan {
     if (groups > 32) return;  // (the exact form's)
     shift = 31 - __clz(32 / groups);
     n = (G & 3) == 0 ? G >> 2 : G;
-    even = (groups & (groups - 1)) == 0 && (G & 3) == 0 && (E & 127) == 0;
     const int unit = 1 << shift, g = lane >> shift, sub = lane & (unit - 1);
     start = sub + unit * g;
     if (start >= n) start = sub + unit * (g % ((n + unit - 1) >> shift));
@@ -249,7 +250,7 @@ __device__ __noinline__ uint32_t open_groups(const float* row, const float* __re
 
 // One token, decided as described above; false: not decided.  Lane j < k returns
 // slot j's expert and score.  `row` is the staged row.
-template <int NK, bool SOFTMAX, bool BIAS, bool GROUPED, bool FULL>
+template <int NK, bool SOFTMAX, bool BIAS, int GROUPED, bool FULL>
 __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k,
                                                   const ScoreRule& R, const GroupPlan& L, int lane,
                                                   uint32_t vmask, const float* __restrict__ bias,
@@ -311,9 +312,9 @@ __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k
       b = fmaxf(b, fminf(a, v));
       a = max2_nan(a, v);
     };
-    if (FULL && NK >= 4 && L.even) {
-      // (each step straight-line: the general walk below cost 24 of 96 us at 65536 x 512)
-      constexpr int kSteps = NK >= 4 ? NK / 4 : 1;
+    if constexpr (GROUPED == kEvenGroups) {
+      // straight-line: the general walk below cost 24 of 96 us at 65536 x 512
+      constexpr int kSteps = NK / 4;
       const float4* part = reinterpret_cast<const float4*>(skey + g * G) + sub;
 #pragma unroll
       for (int it = 0; it < kSteps; ++it) {
@@ -360,7 +361,7 @@ __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k
     // (maxima on order codes: the integer reduction is one instruction)
     const float big = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(mag)));
     uint32_t kept = 0u, best, next;
-    if (R.groups <= 8) {
+    if (GROUPED == kEvenGroups && R.groups <= 8) {
       // a group's rank: each of its lanes compares it with every unit-th group
       const uint32_t scode = order_code(score), mine = unit == 32 ? kFull : (1u << unit) - 1u;
       int rank = 0;
@@ -513,7 +514,7 @@ __host__ __device__ constexpr size_t warp_bytes(int E, bool keys) {
 
 constexpr int scored_min_blocks(int nk) { return nk <= 8 ? 8 : nk == 16 ? 7 : 4; }
 
-template <int NK, bool SOFTMAX, bool BIAS, bool GROUPED, bool FULL>
+template <int NK, bool SOFTMAX, bool BIAS, int GROUPED, bool FULL>
 __global__ void __launch_bounds__(kScoredWarps * 32, scored_min_blocks(NK))
     route_scored_kernel(const float* __restrict__ logits, const float* __restrict__ bias, int T,
                         int E, int k, const __grid_constant__ ScoreRule R, int vec,
@@ -744,18 +745,26 @@ namespace {
 using ScoredKernel = void (*)(const float*, const float*, int, int, int, ScoreRule, int, int32_t*,
                               float*, WsHeader*);
 
-template <int NK, bool SOFTMAX, bool BIAS, bool GROUPED>
-ScoredKernel scored_kernel(int E) {
-  return E == 32 * NK ? route_scored_kernel<NK, SOFTMAX, BIAS, GROUPED, true>
-                      : route_scored_kernel<NK, SOFTMAX, BIAS, GROUPED, false>;
+template <int NK, bool SOFTMAX, bool BIAS>
+ScoredKernel scored_kernel(int E, int groups) {  // 0: not scored by groups
+  const bool full = E == 32 * NK;
+  if (groups == 0)
+    return full ? route_scored_kernel<NK, SOFTMAX, BIAS, kNoGroups, true>
+                : route_scored_kernel<NK, SOFTMAX, BIAS, kNoGroups, false>;
+  if constexpr (NK >= 4) {
+    if (full && groups <= 32 && (groups & (groups - 1)) == 0 && (E / groups) % 4 == 0)
+      return route_scored_kernel<NK, SOFTMAX, BIAS, kEvenGroups, true>;
+  }
+  return full ? route_scored_kernel<NK, SOFTMAX, BIAS, kAnyGroups, true>
+              : route_scored_kernel<NK, SOFTMAX, BIAS, kAnyGroups, false>;
 }
-template <bool SOFTMAX, bool BIAS, bool GROUPED>
-ScoredKernel scored_kernel(int E) {
-  return E <= 64    ? scored_kernel<2, SOFTMAX, BIAS, GROUPED>(E)
-         : E <= 128 ? scored_kernel<4, SOFTMAX, BIAS, GROUPED>(E)
-         : E <= 256 ? scored_kernel<8, SOFTMAX, BIAS, GROUPED>(E)
-         : E <= 512 ? scored_kernel<16, SOFTMAX, BIAS, GROUPED>(E)
-                    : scored_kernel<32, SOFTMAX, BIAS, GROUPED>(E);
+template <bool SOFTMAX, bool BIAS>
+ScoredKernel scored_kernel(int E, int groups) {
+  return E <= 64    ? scored_kernel<2, SOFTMAX, BIAS>(E, groups)
+         : E <= 128 ? scored_kernel<4, SOFTMAX, BIAS>(E, groups)
+         : E <= 256 ? scored_kernel<8, SOFTMAX, BIAS>(E, groups)
+         : E <= 512 ? scored_kernel<16, SOFTMAX, BIAS>(E, groups)
+                    : scored_kernel<32, SOFTMAX, BIAS>(E, groups);
 }
 
 }  // namespace
@@ -764,18 +773,12 @@ cudaError_t launch_route_scored(const LaunchEnv& env, const float* logits, const
                                 int E, int k, const ScoreRule& rule, int32_t* ids, float* gates,
                                 WsHeader* hdr) {
   const bool grouped = rule.top_groups < rule.groups;
-  const int form = (rule.softmax ? 4 : 0) + (bias != nullptr ? 2 : 0) + (grouped ? 1 : 0);
-  ScoredKernel kernel = nullptr;
-  switch (form) {
-    case 0: kernel = scored_kernel<false, false, false>(E); break;
-    case 1: kernel = scored_kernel<false, false, true>(E); break;
-    case 2: kernel = scored_kernel<false, true, false>(E); break;
-    case 3: kernel = scored_kernel<false, true, true>(E); break;
-    case 4: kernel = scored_kernel<true, false, false>(E); break;
-    case 5: kernel = scored_kernel<true, false, true>(E); break;
-    case 6: kernel = scored_kernel<true, true, false>(E); break;
-    default: kernel = scored_kernel<true, true, true>(E); break;
-  }
+  const int groups = grouped ? rule.groups : 0;
+  const ScoredKernel kernel =
+      rule.softmax ? (bias != nullptr ? scored_kernel<true, true>(E, groups)
+                                      : scored_kernel<true, false>(E, groups))
+                   : (bias != nullptr ? scored_kernel<false, true>(E, groups)
+                                      : scored_kernel<false, false>(E, groups));
   const int vec = (E % 4) == 0 && (reinterpret_cast<uintptr_t>(logits) % 16) == 0;
   const size_t smem = kScoredWarps * warp_bytes(E, grouped);
   int per_sm = 1;
