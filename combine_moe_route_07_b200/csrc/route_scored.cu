@@ -611,9 +611,10 @@ __device__ __forceinline__ float merge_slots(float d, int& e, int lane) {
 // The gradient lives on the chosen experts alone (every rule but the full softmax).
 // W lanes a token, two tokens a warp where k <= 16.  The row is zeroed by wide stores
 // that wait for nothing, the k values follow them (the warp's stores are ordered by
-// the barrier between): store-bound, 4E bytes a token.
+// the barrier between): store-bound, 4E bytes a token.  32768 x 256, k 8: 10.2 us, in 36
+// registers instead of 32 (fewer warps to hide the loads' latency) 10.9.
 template <int W>
-__global__ void __launch_bounds__(kBackWarps * 32)
+__global__ void __launch_bounds__(kBackWarps * 32, 8)
     route_scored_backward_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids,
                                  const float* __restrict__ grad_gates, int T, int E, int k,
                                  const __grid_constant__ ScoreRule R,
