@@ -231,6 +231,44 @@ def test_gradient_edges():
         assert (got.abs() <= 2.0 ** -100).all()
 
 
+@pytest.mark.parametrize("E,groups,k", [(64, 2, 6), (128, 4, 8), (256, 8, 8), (512, 8, 10), (512, 16, 9),
+                                        (1024, 32, 8), (512, 2, 32), (160, 5, 6), (96, 8, 5), (80, 16, 4)])
+@pytest.mark.parametrize("func", ["softmax", "sigmoid"])
+def test_groups_closer_than_fp32_are_decided_exactly(func, E, groups, k):
+    """Every group holds the same values in another order, some moved by one fp32 step: which groups are
+    kept is a matter of the last bits, or of the lower index."""
+    g = torch.Generator().manual_seed(E + groups)
+    T, G = 64, E // groups
+    base = torch.randn(T, 1, G, generator=g).expand(T, groups, G)
+    order = torch.rand(T, groups, G, generator=g).argsort(2)
+    logits = torch.gather(base, 2, order).reshape(T, E)
+    moved = torch.rand(T, E, generator=g) < 0.2
+    logits = torch.where(moved, torch.nextafter(logits, torch.full_like(logits, 9.0)), logits)
+    top = max(1, groups // 2)
+    for gt in (1, 2):
+        if top * G >= k:
+            for bias in (None, torch.full((E,), 0.125)):
+                _compare(logits, k, func, True, groups, top, gt, 1.0, bias)
+
+
+@pytest.mark.parametrize("E,groups", [(64, 8), (128, 4), (256, 8), (512, 8), (512, 32), (160, 5)])
+def test_nan_in_any_group_is_reported(E, groups):
+    m = _mod()
+    from combine_moe_route_07_b200 import _binding
+    logits = _randn(12, E, seed=groups)
+    for e in range(0, E, max(1, E // 13)):
+        bad = logits.clone()
+        bad[5] -= 4.0 * (torch.arange(E) // (E // groups) == e * groups // E)  # its group is not among the best
+        bad[5, e] = float("nan")
+        for func in ("sigmoid", "softmax"):
+            ids, gates, ws = _run(bad, 4, func, True, groups, groups // 2, 2, check=False)
+            assert m.moe_get_device_error(ws) == (_binding.MOE_ERR_DEVICE_NAN, 5)
+            assert ids[5].tolist() == [0, 1, 2, 3] and (gates[5] == 0).all()
+            keep = [t for t in range(12) if t != 5]
+            want, _, _ = ref.route(logits[keep], 4, func, True, groups, groups // 2, 2)
+            assert torch.equal(ids[keep].long(), want)
+
+
 def test_gradient_of_scores_below_fp32():
     """Sigmoid scores whose chosen sum is near or below fp32's smallest number: the gates are quotients
     of them all the same, and so are the gradients."""
