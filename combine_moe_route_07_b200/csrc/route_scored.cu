@@ -612,12 +612,44 @@ __device__ __forceinline__ float merge_slots(float d, int& e, int lane) {
   return d;
 }
 
+// The largest of row[0..E-1] over the W lanes of its token (NaN passed over).
+template <int W>
+__device__ __forceinline__ float row_max(const float* __restrict__ row, int E, int j, bool vec) {
+  float m = -INFINITY;
+  if (vec) {
+    for (int i = j * 4; i < E; i += W * 4) {
+      const float4 v = __ldg(reinterpret_cast<const float4*>(row + i));
+      m = fmaxf(m, fmaxf(fmaxf(v.x, v.y), fmaxf(v.z, v.w)));
+    }
+  } else {
+    for (int i = j; i < E; i += W) m = fmaxf(m, __ldg(row + i));
+  }
+  return lanes_max<W>(m);
+}
+
+// Whether the scores of a token's chosen experts (logit l, one a lane; -INFINITY: none)
+// sum to zero in binary64, formed as the route's exact form forms them.  M: the row's
+// largest logit.  Called by whole warps.
+template <int W>
+__device__ __noinline__ bool scores_vanish(const float* __restrict__ row, int E, float M, float l,
+                                           int j, bool token) {
+  double s = 0.0;
+  if (token)
+    for (int i = j; i < E; i += W) s += exp((double)__ldg(row + i) - (double)M);
+  const double inv_sum = 1.0 / lanes_sum<W>(s);
+  const double mine = l > -INFINITY ? score_d((double)l, (double)M, inv_sum, true) : 0.0;
+  return lanes_sum<W>(mine) == 0.0;
+}
+
 // The gradient lives on the chosen experts alone (every rule but the full softmax).
 // W lanes a token, two tokens a warp where k <= 16.  The row is zeroed by wide stores
 // that wait for nothing, the k values follow them (the warp's stores are ordered by
-// the barrier between): store-bound, 4E bytes a token.  32768 x 256, k 8: 10.2 us, in 36
-// registers instead of 32 (fewer warps to hide the loads' latency) 10.9.
-template <int W>
+// the barrier between): store-bound, 4E bytes a token (softmax: 4E read as well, since
+// only the row's largest logit tells whether the chosen scores vanish).  32768 x 256,
+// k 8, over buffers larger than the L2: sigmoid 13.5 us, softmax 15.4 (13.4 without the
+// row); 65536 x 512, k 10, softmax: 55 us, 4.9 TB/s.  On one buffer sigmoid takes 10.2
+// us, in 36 registers instead of 32 (fewer warps to hide the loads' latency) 10.9.
+template <int W, bool SOFTMAX>
 __global__ void __launch_bounds__(kBackWarps * 32, 8)
     route_scored_backward_kernel(const float* __restrict__ logits, const int32_t* __restrict__ ids,
                                  const float* __restrict__ grad_gates, int T, int E, int k,
@@ -638,7 +670,7 @@ __global__ void __launch_bounds__(kBackWarps * 32, 8)
     }
     float* out = grad_logits + (size_t)t0 * E;
     const int n = (min(T - t0, kTok)) * E;
-    if (vec) {
+    if ((vec & 1) != 0) {
       for (int i = lane * 4; i < n; i += 128)
         *reinterpret_cast<float4*>(out + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     } else {
@@ -651,12 +683,22 @@ __global__ void __launch_bounds__(kBackWarps * 32, 8)
     const float l = e >= 0 ? __ldg(logits + (size_t)t * E + e) : 0.0f;
     up = e >= 0 ? (float)((double)up * R.scale) : 0.0f;
     float d;
-    if (R.softmax) {  // renormalised: the softmax of the chosen
-      // (a bias can choose masked experts alone: gates of zero, no gradient)
-      const float m = lanes_max<W>(e >= 0 ? l : -INFINITY);
-      const float x = e >= 0 && l != -INFINITY ? expf(l - m) : 0.0f;
+    if (SOFTMAX) {  // renormalised: the softmax of the chosen
+      // A bias, or few unmasked experts, can choose scores that are all zero in binary64
+      // (masks of -inf or any finite value, logits 745 below the largest): the gates are
+      // zero there, whatever the logits, and there is no gradient.
+      const float* row = logits + (size_t)min(t, T - 1) * E;
+      const float M = row_max<W>(row, E, j, (vec & 2) != 0);
+      const float c = e >= 0 ? l : -INFINITY;
+      const float m = lanes_max<W>(c);
+      const float x = c != -INFINITY ? expf(l - m) : 0.0f;
       const float sum = lanes_sum<W>(x);
-      const float p = sum != 0.0f ? x * (1.0f / sum) : 0.0f;
+      float p = sum != 0.0f ? x * (1.0f / sum) : 0.0f;
+      const bool far = m > -INFINITY && m - M < -600.0f;
+      if (__any_sync(kFull, far)) {
+        const bool gone = scores_vanish<W>(row, E, M, c, j, far);
+        if (far && gone) p = 0.0f;
+      }
       d = p * (up - lanes_sum<W>(up * p));
     } else {
       // sigmoid(l) and 1 - sigmoid(l), both without cancellation
@@ -799,10 +841,15 @@ cudaError_t launch_route_scored_backward(const LaunchEnv& env, const float* logi
                                          const int32_t* ids, const float* grad_gates, int T, int E,
                                          int k, const ScoreRule& rule, float* grad_logits,
                                          WsHeader* hdr) {
-  const int vec = (E % 4) == 0 && (reinterpret_cast<uintptr_t>(grad_logits) % 16) == 0;
+  const auto wide = [&](const float* p) { return E % 4 == 0 && reinterpret_cast<uintptr_t>(p) % 16 == 0; };
+  const int vec = (wide(grad_logits) ? 1 : 0) | (wide(logits) ? 2 : 0);
   const bool dense = rule.softmax && !rule.renorm;
   const size_t smem = dense ? sizeof(float) * kBackWarps * (size_t)((E + 3) / 4 * 4) : 0;
-  const auto chosen = k <= 16 ? route_scored_backward_kernel<16> : route_scored_backward_kernel<32>;
+  const auto chosen =
+      rule.softmax
+          ? (k <= 16 ? route_scored_backward_kernel<16, true> : route_scored_backward_kernel<32, true>)
+          : (k <= 16 ? route_scored_backward_kernel<16, false>
+                     : route_scored_backward_kernel<32, false>);
   int per_sm = 1;
   cudaError_t err = blocks_per_sm(
       dense ? (const void*)route_softmax_backward_kernel : (const void*)chosen, kBackWarps * 32, smem,
@@ -814,7 +861,7 @@ cudaError_t launch_route_scored_backward(const LaunchEnv& env, const float* logi
   if (dense)
     return launch_pdl(env, route_softmax_backward_kernel, dim3((unsigned)grid),
                       dim3(kBackWarps * 32), smem, logits, ids, grad_gates, T, E, k, rule.scale,
-                      grad_logits, vec, hdr);
+                      grad_logits, vec & 1, hdr);
   return launch_pdl(env, chosen, dim3((unsigned)grid), dim3(kBackWarps * 32), 0, logits, ids,
                     grad_gates, T, E, k, rule, grad_logits, vec, hdr);
 }

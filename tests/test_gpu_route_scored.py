@@ -377,3 +377,42 @@ def test_no_tokens_and_wrong_arguments():
         m.moe_route_scored(shape, logits.cpu(), m.ScoreRule(), ws=ws)
     with pytest.raises(ValueError):
         m.moe_route_scored(shape, logits.t().contiguous().t(), m.ScoreRule(), ws=ws)
+
+
+def _masked_choice(T, E, W, value, seed):
+    """Logits whose first W experts are far below the others in all but every third token, and a bias that
+    chooses just those W."""
+    logits = _randn(T, E, seed=seed)
+    low = torch.arange(T) % 3 != 2
+    logits[low, :W] = value if abs(value) > 1e6 else logits[low, :W] + value
+    bias = torch.zeros(E)
+    bias[:W] = 3.0 - 0.01 * torch.arange(W)
+    return logits, bias
+
+
+@pytest.mark.parametrize("value", [-1e9, torch.finfo(torch.float32).min, -800.0, -600.0, -90.0])
+@pytest.mark.parametrize("E,W", [(48, 4), (51, 5), (256, 16), (64, 20), (1024, 32)])
+@pytest.mark.parametrize("shift", [0.0, 300.0])
+def test_gradient_where_the_chosen_scores_vanish(value, E, W, shift):
+    """Experts masked with a finite value, chosen by a bias: where the scores are zero in binary64 the gates
+    are zero whatever the logits, and so are the gradients.  Scores that binary64 still holds (600 below the
+    largest logit) have gates and gradients like any others.  Quotients: expf of a difference of logits below
+    8 (2^-21) and fp32 sums of up to 32 terms (2^-19), as in the other gradient tests."""
+    m = _mod()
+    T = 41
+    logits, bias = _masked_choice(T, E, W, value, E + W)
+    logits = logits + shift
+    up = _randn(T, W, seed=2)
+    want, g, _ = ref.route(logits, W, "softmax", True, bias=bias)
+    ids, gates, _ = _run(logits, W, "softmax", True, bias=bias)
+    assert torch.equal(ids.long(), want)
+    gone = (g == 0).all(1)
+    assert int(gone.sum()) == (T - T // 3 if value <= -800.0 else 0)
+    assert (gates[gone] == 0).all()
+    shape = m.MoeShape(tokens=T, hidden=8, experts=E, k=W, ranks=1, renorm=True)
+    got = m.moe_route_scored_backward(shape, logits.cuda(), m.ScoreRule("softmax"), ids.cuda(), up.cuda(),
+                                      ws=m.Workspace(shape)).cpu().double()
+    part = g * (up.double() - (g * up.double()).sum(1, keepdim=True))
+    whole = torch.zeros(T, E, dtype=torch.float64).scatter_(1, want, part)
+    assert ((got - whole).abs() <= 2.0 ** -18 * up.double().abs().sum(1, keepdim=True)).all()
+    assert (got[gone] == 0).all()
