@@ -554,6 +554,9 @@ __global__ void __launch_bounds__(kScoredWarps * 32, scored_min_blocks(NK))
     double s = 0.0;
     bool ok = fast && scored_token_fast<NK, SOFTMAX, BIAS, GROUPED, FULL>(
                           rows + turn * stride, E, k, R, plan, lane, vmask, bias, skey, C, e, s);
+    // Scores at the end of binary64's range: their quotients depend on how each was
+    // rounded there, which is for the exact form to say (it divides by the row's sum).
+    if (SOFTMAX && BIAS && ok && R.renorm && !__any_sync(kFull, s > 1e-280)) ok = false;
     if (!ok) {
       // the exact form's keys take both staged rows: the next one is staged again
       asm volatile("cp.async.wait_group 0;" ::: "memory");

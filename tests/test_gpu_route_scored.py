@@ -416,3 +416,17 @@ def test_gradient_where_the_chosen_scores_vanish(value, E, W, shift):
     whole = torch.zeros(T, E, dtype=torch.float64).scatter_(1, want, part)
     assert ((got - whole).abs() <= 2.0 ** -18 * up.double().abs().sum(1, keepdim=True)).all()
     assert (got[gone] == 0).all()
+
+
+@pytest.mark.parametrize("E,W", [(48, 4), (300, 16), (1000, 24)])
+def test_gates_of_scores_at_the_end_of_binary64(E, W):
+    """Chosen scores that are binary64's last few subnormals, or the first that it loses: the gates are
+    quotients of those numbers, as everywhere."""
+    T = 200
+    logits = _randn(T, E, seed=E, scale=0.3)
+    logits[:, :W] = torch.linspace(-725.0, -748.0, T)[:, None] + _randn(T, W, seed=1, scale=0.3)
+    bias = torch.zeros(E)
+    bias[:W] = 3.0 - 0.01 * torch.arange(W)
+    want, g, _ = ref.route(logits, W, "softmax", True, bias=bias)
+    assert (g == 0).all(1).any() and not (g == 0).all(1).all()
+    _compare(logits, W, "softmax", True, bias=bias)
