@@ -762,6 +762,8 @@ __global__ void __launch_bounds__(kBackWarps * 32)
       m = fmaxf(m, l);
     }
     m = lanes_max<32>(m);
+    // (a row whose mask leaves nothing has gates of zero: zeros here too, not NaN)
+    if (m == -INFINITY) m = 0.0f;
     float sum = 0.0f;
     for (int i = lane; i < E; i += 32) {
       const float p = expf(srow[i] - m);
@@ -769,7 +771,8 @@ __global__ void __launch_bounds__(kBackWarps * 32)
       sum += p;
     }
     __syncwarp();
-    const float inv = 1.0f / lanes_sum<32>(sum);
+    sum = lanes_sum<32>(sum);
+    const float inv = sum != 0.0f ? 1.0f / sum : 0.0f;
     float d = e >= 0 ? up * (srow[e] * inv) : 0.0f;
     const float dot = lanes_sum<32>(d);  // sum of up * p over the chosen
     d = merge_slots<32>(d, e, lane);

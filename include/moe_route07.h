@@ -343,7 +343,8 @@ moe_status_t moe_route_scored(const moe_shape_t* shape, const float* logits, con
  * itself has none).  ids are the chosen experts, grad_gates fp32 [T,k];
  * grad_logits fp32 [T,E] is written whole (zeros where there is no gradient).
  * A token whose chosen scores sum to 0 with MOE_F_RENORM, as the route forms
- * them (binary64), has gates of zero and no gradient.
+ * them (binary64), has gates of zero and no gradient; nor has a token whose
+ * softmax logits are all -inf.
  * An expert that appears in two slots of a token gets the sum of their parts;
  * an id outside [0,E) sets MOE_ERR_DEVICE_RANGE and its slot has no gradient
  * and no share in the renormalisation. */

@@ -430,3 +430,24 @@ def test_gates_of_scores_at_the_end_of_binary64(E, W):
     want, g, _ = ref.route(logits, W, "softmax", True, bias=bias)
     assert (g == 0).all(1).any() and not (g == 0).all(1).all()
     _compare(logits, W, "softmax", True, bias=bias)
+
+
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("E,k", [(40, 4), (37, 20), (1024, 32)])
+def test_gradient_of_a_row_whose_mask_leaves_nothing(renorm, E, k):
+    """Every logit -inf: the route reports the token and gives it gates of zero; it has no gradient, and the
+    tokens beside it have theirs."""
+    m = _mod()
+    T = 9
+    logits, up = _randn(T, E, seed=3), _randn(T, k, seed=4)
+    logits[[0, 4]] = -float("inf")
+    ids = torch.arange(k, dtype=torch.int32).expand(T, k).contiguous()
+    shape = m.MoeShape(tokens=T, hidden=8, experts=E, k=k, ranks=1, renorm=renorm)
+    call = lambda l: m.moe_route_scored_backward(  # noqa: E731
+        shape, l.cuda(), m.ScoreRule("softmax"), ids.cuda(), up.cuda(), ws=m.Workspace(shape)).cpu()
+    got = call(logits)
+    assert (got[[0, 4]] == 0).all()
+    keep = [t for t in range(T) if t not in (0, 4)]
+    other = logits.clone()
+    other[[0, 4]] = 1.0
+    assert torch.equal(got[keep], call(other)[keep]) and (got[keep] != 0).any()
