@@ -86,10 +86,12 @@ __device__ __forceinline__ void st16(void* p, const uint4& v) {
   *reinterpret_cast<uint4*>(p) = v;
 }
 
-// 2^x within 2 units in the last place and 1/x within 1, subnormals flushed; the
-// logistic function from them (within 2^-21 of itself for |x| < 8, 2^-18 for |x| < 64:
-// the rounding of x log2(e) grows with x).  The library's fast forms handle subnormals
-// too, at about three times the instructions.
+// 2^x within 2^-22 of itself and 1/x within 2^-23, subnormals flushed; the logistic
+// function from them, within (7 + 1.23 |x|) 2^-24 of itself (x log2(e) is rounded and
+// log2(e) is, which the exponential turns into 1.23 |x| steps of 2^-24; 4 for 2^x, 1 for
+// the addition, 2 for the reciprocal): 2^-19.9 at |x| = 8, 2^-17.5 at 64.  Below -87.3
+// it is 0.  The library's fast forms handle subnormals too, at about three times the
+// instructions.
 __device__ __forceinline__ float ex2_f(float x) {
   float r;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));

@@ -181,13 +181,20 @@ __device__ __noinline__ bool scored_token_slow(const float* row, const float* bi
   return scored_token_exact(row, bias, E, k, R, lane, key, sel_e, sel_s);
 }
 
-// How far a binary32 key can be from its binary64 value.  A score of its own is within
-// 2^-21 (2^x is off by 2^-22, its argument's rounding is damped by the score, the
-// reciprocal adds 2^-23), one addition adds 2^-24 of the key.  The softmax's sum is
-// off by at most 1.5e-6 of itself (14 additions, 2^x and its arguments, the reciprocal),
-// alike for every score of the token: two keys move apart by that times the difference
-// of their scores, which is at most 1, and by 2^-22 of the scores' sum: less than the
-// 2e-6 by which two bounds keep keys apart.
+// How far a binary32 key can be from its binary64 value, in steps u = 2^-24.
+// Sigmoid: 2^x is off by 4 u of itself and its argument by 1.23 u |l|; the score s takes
+// s (1 - s) of that (at most 1 u and 0.28 u), 1 u for the addition, 2 u for the reciprocal:
+// 4.3 u, 2.6e-7.
+// Softmax: 2^x is off by 4 u and its argument, d = l - m times log2 e, by 1.23 u |d|, of
+// which the score p takes p and p |d| < 0.37: 4.9 u for two scores, which sum to at most 1.
+// (Without a bias by 2.23 u |d|, but nothing else is: 5.7 u.)  The sum is off by 4 u, 1.23 u
+// times the scores' mean |d| (at most 4.45 over 1024 scores: one ahead of equal others),
+// 10 u for its additions and 3 u for the reciprocal, alike for every score of the token: two
+// keys move apart by the difference of their scores, at most 1, times these 22.5 u.  27.4 u
+// or 1.7e-6 in all, below the 2e-6 by which two bounds keep keys apart.
+// One addition adds 1 u of the key.
+// The gates of the full softmax are binary64 exponentials times a reciprocal of which 5 u
+// are its additions and 1 u its rounding, and are rounded once: 16.5 u, 9.8e-7.
 __device__ __forceinline__ float key_bound(float v) { return 1.0e-6f + 2.5e-7f * fabsf(v); }
 
 // What the group scoring needs of the sizes, computed once: unit = 1 << shift lanes a
@@ -218,6 +225,39 @@ __device__ __noinline__ double softmax_scale_d(const float* row, int E, double m
   double s = 0.0;
   for (int e = lane; e < E; e += 32) s += exp((double)row[e] - m);
   return 1.0 / wsum_d(s);
+}
+
+// f(LO) + .. + f(LO + N - 1), N a power of two, added pairwise.
+template <int LO, int N, typename F>
+__device__ __forceinline__ float sum_tree(const F& f) {
+  if constexpr (N == 1)
+    return f(LO);
+  else
+    return sum_tree<LO, N / 2>(f) + sum_tree<LO + N / 2, N / 2>(f);
+}
+
+// 1 / (sum of the lanes' values, each in [0, 33] and together at least 0.9), to one
+// rounding.  The values are added as whole numbers of 2^-20 and, of the rest, of 2^-42:
+// exact but for 32 * 2^-42, and the reduction of an integer is one instruction.
+__device__ __forceinline__ float lanes_total_inverse(float v) {
+  const float scaled = v * 0x1p20f;
+  const uint32_t whole = __float2uint_rz(scaled);
+  const uint32_t rest = __float2uint_rz((scaled - (float)whole) * 0x1p22f);
+  const uint32_t hi = __reduce_add_sync(kFull, whole), lo = __reduce_add_sync(kFull, rest);
+  const float a = (float)hi;
+  const float b = fmaf((float)lo, 0x1p-22f, (float)(int)(hi - (uint32_t)a));  // a + b: the sum
+  const float r = rcp_f(a);
+  return fmaf(r, fmaf(-b, r, fmaf(-a, r, 1.0f)), r) * 0x1p20f;
+}
+
+// A softmax's powers are 2^(l log2 e - c), c = m log2 e rounded, up to this |m|.
+constexpr float kShift = 32768.0f;
+// 2^(m log2 e - c) - 1: what the reciprocal of their sum lacks of that of the sum of
+// e^(l - m).  (|m log2 e - c| < 2^-8: the third power of its series is 2^-35.)
+__device__ __forceinline__ float shift_lost(float m) {
+  const float lost =
+      fabsf(m) <= kShift ? 0.693147181f * fmaf(m, kLog2e, -(m * kLog2e)) : 0.0f;
+  return lost * fmaf(lost, fmaf(lost, 0.166666667f, 0.5f), 1.0f);
 }
 
 // The kept groups' bits by binary64 scores, where binary32 leaves them open:
@@ -267,6 +307,8 @@ __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k
 #pragma unroll
   for (int i = 0; i < NK; ++i) key[i] = valid(i) ? row[lane + 32 * i] : -INFINITY;
   float m = 0.0f, scale = 1.0f;  // softmax: largest logit, and what 2^.. is multiplied with
+  float from = 0.0f, c = 0.0f;
+  auto power = [&](float l) { return ex2_f(fmaf(l - from, kLog2e, -c)); };  // e^(l - m)
   if (SOFTMAX) {
     m = key[0];
 #pragma unroll
@@ -274,15 +316,25 @@ __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k
     if (__any_sync(kFull, m != m)) return false;
     m = code_float(__reduce_max_sync(kFull, order_code(m)));
     if (!(fabsf(m) < INFINITY)) return false;  // a row without a finite maximum
+    from = m;
     if (BIAS || !R.renorm) {
-      // four partial sums: at most 14 roundings of 2^-24 with the shuffles
-      float p4[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      // The argument (l - m) log2 e with one rounding: less c, which is m log2 e rounded (all
+      // powers and their sum are off by the same factor, see shift_lost); from 2^15 on,
+      // where that would be too much, l - m is exact wherever 2^.. is not 0.  A lane's terms
+      // are added pairwise: log2(NK) <= 5 roundings.  Where the sum goes into the gates, the
+      // lanes' parts are added without any (for the keys alone too, 65536 x 512 took 69 us
+      // instead of 66).
+      const bool small = fabsf(m) <= kShift;
+      from = small ? 0.0f : m;
+      c = small ? m * kLog2e : 0.0f;
+      float part = sum_tree<0, NK>([&](int i) { return power(key[i]); });
+      if (R.renorm) {  // scales the keys alone
 #pragma unroll
-      for (int i = 0; i < NK; ++i) p4[i & 3] += ex2_f((key[i] - m) * kLog2e);
-      float part = (p4[0] + p4[1]) + (p4[2] + p4[3]);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kFull, part, o);
-      scale = __fdividef(1.0f, part);
+        for (int o = 16; o > 0; o >>= 1) part += __shfl_xor_sync(kFull, part, o);
+        scale = rcp_f(part);
+      } else {
+        scale = lanes_total_inverse(part);
+      }
     }
   }
   // the key of expert e with logit l
@@ -290,7 +342,7 @@ __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k
     float v;
     if (SOFTMAX) {
       if (raw) return l;
-      v = ex2_f((l - m) * kLog2e);
+      v = power(l);
       return BIAS ? fmaf(v, scale, __ldg(bias + e)) : v;
     }
     v = sigmoid_f(l);
@@ -485,7 +537,7 @@ __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k
   if (lane < k) {
     sel_e = C->expert[C->slot[lane]];
     sel_s = score_d((double)row[sel_e], (double)m, 1.0, SOFTMAX);
-    if (SOFTMAX && !R.renorm) sel_s *= (double)scale;
+    if (SOFTMAX && !R.renorm) sel_s *= (double)scale * (1.0 + (double)shift_lost(m));
   }
   __syncwarp();
   return true;

@@ -451,3 +451,34 @@ def test_gradient_of_a_row_whose_mask_leaves_nothing(renorm, E, k):
     other = logits.clone()
     other[[0, 4]] = 1.0
     assert torch.equal(got[keep], call(other)[keep]) and (got[keep] != 0).any()
+
+
+@pytest.mark.parametrize("with_bias", [False, True])
+@pytest.mark.parametrize("E", [64, 256, 512, 1024])
+def test_softmax_gates_over_nearly_equal_logits(E, with_bias):
+    """Gates without renormalisation where every rounding of the sum's terms goes one way: one expert
+    ahead of E - 1 equal ones."""
+    T = 4096
+    ahead = torch.linspace(0.0, 12.0, T)
+    logits = torch.zeros(T, E)
+    logits[:, 5] = ahead
+    base = _randn(T, 1, seed=E, scale=3.0)
+    bias = 0.01 * _randn(E, seed=1) if with_bias else None
+    _compare(logits + base, 4, "softmax", False, bias=bias)
+    _compare(-logits.flip(1) - base, 4, "softmax", False, bias=bias)
+
+
+@pytest.mark.parametrize("shift", [0.0, -77.7, 313.1, -5001.3, 32760.9, -40000.3, 3e6])
+@pytest.mark.parametrize("renorm", [False, True])
+def test_softmax_of_shifted_logits(shift, renorm):
+    """Rows whose largest logit is far from zero, and a bias that brings their keys within 1e-6 of each
+    other: the choice and the gates are the 64-bit ones of the shifted values."""
+    for E, groups, top, gt in ((64, 1, 1, 1), (256, 8, 4, 2), (512, 1, 1, 1), (100, 4, 2, 1)):
+        T = 300
+        logits = _randn(T, E, seed=E, scale=1.5) + shift
+        _compare(logits, 6, "softmax", renorm, groups, top, gt)
+        s = ref.scores(logits[:1], "softmax")[0]
+        near = (s + 1e-6 * _randn(E, seed=3).double())
+        row = logits[:1].expand(T, E).clone()
+        row[:, 1::2] = row[:, 1::2] + 1e-3 * _randn(T, E // 2, seed=4)  # the sums differ, most keys stay near
+        _compare(row, 6, "softmax", renorm, groups, top, gt, bias=(0.5 - near).float())
