@@ -52,20 +52,13 @@ __device__ __forceinline__ int seg_rows(const ActParams& P, int e, int* off) {
   return r;
 }
 
-// Slope of the activation at z.  gelu: Phi(z) + z phi(z), Phi's tail by the
-// rational approximation 7.1.26 of Abramowitz and Stegun's Handbook (as in the
-// forward product), which shares the exponential with phi.
+// Slope of the activation at z (gelu: Phi(z) + z phi(z)).
 template <int ACT>
 __device__ __forceinline__ float slope(float z) {
   if (ACT == MOE_ACT_RELU) return z > 0.0f ? 1.0f : 0.0f;
   if (ACT == MOE_ACT_GELU) {
-    const float x = fabsf(z) * 0.70710678f, e = ex2_f(x * x * -kLog2e);
-    const float t = rcp_f(fmaf(0.3275911f, x, 1.0f));
-    float q = fmaf(1.061405429f, t, -1.453152027f);
-    q = fmaf(q, t, 1.421413741f);
-    q = fmaf(q, t, -0.284496736f);
-    q = fmaf(q, t, 0.254829592f);
-    const float tail = 0.5f * q * t * e;
+    float e;
+    const float tail = normal_tail(z, &e);
     return fmaf(z * 0.39894228f, e, z < 0.0f ? tail : 1.0f - tail);
   }
   if (ACT == MOE_ACT_SILU || ACT == MOE_ACT_SWIGLU) {

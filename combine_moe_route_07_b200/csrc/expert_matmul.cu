@@ -114,17 +114,10 @@ __device__ __forceinline__ Segment segment(const GemmParams& P, int e, bool tell
   return s;
 }
 
-// gelu(z) = z * Phi(z), Phi by the rational approximation 7.1.26 of Abramowitz
-// and Stegun's Handbook (erfc(x) = (a1 t + .. + a5 t^5) exp(-x^2), t = 1 / (1 +
-// p x), within 1.5e-7): the tail is not a difference of near-equal numbers.
+// gelu(z) = z * Phi(z).
 __device__ __forceinline__ float gelu_f(float z) {
-  const float x = fabsf(z) * 0.70710678f;
-  const float t = rcp_f(fmaf(0.3275911f, x, 1.0f));
-  float q = fmaf(1.061405429f, t, -1.453152027f);
-  q = fmaf(q, t, 1.421413741f);
-  q = fmaf(q, t, -0.284496736f);
-  q = fmaf(q, t, 0.254829592f);
-  const float tail = 0.5f * q * t * ex2_f(x * x * -kLog2e);  // Phi(-|z|)
+  float e;
+  const float tail = normal_tail(z, &e);
   return z * (z < 0.0f ? tail : 1.0f - tail);
 }
 

@@ -433,3 +433,46 @@ def test_wrong_tensors_are_refused():
     with pytest.raises(m.MoeError):  # an activation's gradient needs the pre-activations
         m.moe_expert_matmul_backward(shape, _rows(n, 16, held, 3).cuda(), x, w, lay.counts, lay.expert_off,
                                      ws=ws, act="gelu")
+
+
+def _gelu_tail_tol(z):
+    """Relative error of Phi(-|z|) in fp32: the scaled tail's polynomial (2^-20.7 with its roundings),
+    the exponential (2^-22) and three products (2^-24 each): 17 steps of 2^-24; the exponent z^2 / 2 takes
+    two roundings and a constant off by 0.23 of one, each 2^-24 of it: 1.12 z^2 steps."""
+    return (18.0 + 1.2 * z * z) * 2.0 ** -24
+
+
+def test_gelu_of_far_negative_values():
+    """The tail is held relative to itself: at z = -10 the result is 1e-22, and bf16 shows 2^-8 of that."""
+    m = _mod()
+    F = 4096
+    z = torch.cat([torch.linspace(-13.0, -3.0, F - 1024), torch.linspace(-3.0, 12.0, 1024)])
+    shape = m.MoeShape(tokens=3, hidden=8, experts=1, k=1, ranks=1)
+    x = torch.zeros(3, 8, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(1, F, 8, dtype=torch.bfloat16, device="cuda")
+    got = m.moe_expert_matmul(shape, x, w, ws=m.Workspace(shape), act="gelu", bias=z[None].cuda())
+    zd = z.double()
+    want = 0.5 * zd * torch.erfc(-zd / 2.0 ** 0.5)
+    tol = (U + _gelu_tail_tol(zd) * (1 + U)) * want.abs()
+    for row in got.cpu().double():
+        assert ((row - want).abs() <= tol).all()
+
+
+def test_gelu_slope_of_far_negative_values():
+    """The bias gradient of one row is the slope in fp32, before any rounding to bf16."""
+    m = _mod()
+    F = 4096
+    z = torch.cat([torch.linspace(-13.0, -3.0, F - 1024), torch.linspace(-3.0, 12.0, 1024)]).to(torch.bfloat16)
+    shape = m.MoeShape(tokens=1, hidden=8, experts=1, k=1, ranks=1)
+    x = torch.ones(1, 8, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(1, F, 8, dtype=torch.bfloat16, device="cuda")
+    got = m.moe_expert_matmul_backward(shape, torch.ones(1, F, dtype=torch.bfloat16, device="cuda"), x, w,
+                                       ws=m.Workspace(shape), act="gelu", pre=z[None].cuda(), need_x=False,
+                                       need_bias=True)
+    zd = z.double()
+    phi, Phi = torch.exp(-0.5 * zd * zd) / (2.0 * torch.pi) ** 0.5, 0.5 * torch.erfc(-zd / 2.0 ** 0.5)
+    want, mag = Phi + zd * phi, Phi + zd.abs() * phi
+    err = (got.grad_bias[0].cpu().double() - want).abs()
+    assert (err <= _gelu_tail_tol(zd) * mag).all()
+    off = (got.grad_pre[0].cpu().double() - want).abs()
+    assert (off <= U * want.abs() + (1 + U) * _gelu_tail_tol(zd) * mag).all()
