@@ -206,9 +206,9 @@ cudaError_t launch_combine_backward(const LaunchEnv& env, const void* grad_out, 
                                     const int32_t* dst_pos, const float* gates, int T, int H, int k,
                                     int64_t N, void* grad_y, float* grad_gates, WsHeader* hdr);
 
-// The experts' products.  assignments bounds the rows that hold a token (T*k,
-// or E*C with a capacity, if smaller): grids are sized from it, the segments
-// themselves are read on the device.
+// The experts' products.  assignments = T*k bounds the rows that hold a token, with a
+// capacity too (which may leave far fewer): grids, the choice of tile heights and the bias
+// gradient's scratch are sized from it, the segments themselves are read on the device.
 struct ExpertMatmul {
   const void* x;
   const void* w;

@@ -23,8 +23,17 @@
 //      of them, usually) are compacted, one a lane;
 //   3. they are ranked by their binary32 keys; where two neighbours among the k
 //      best are closer than the bound, by their binary64 keys, ties by expert.
-// A token whose candidates stay open (masks that leave less than k finite keys,
-// NaN, more than 32 candidates) is decided in binary64 throughout, out of line.
+// A token whose candidates stay open is decided in binary64 throughout, out of line:
+//   - masks that leave less than k finite keys, and NaN;
+//   - more than 32 keys within the bound of the k-th largest lane maximum: keys closer
+//     together than 1e-6 (sigmoid scores all below that or saturated, logits below -14 or
+//     above 16; a biased softmax over logits equal to 1e-3), or k above about 20, where
+//     the k-th lane maximum lies far below the k-th key;
+//   - more than 32 groups.
+// A whole batch of them costs what the definition taken literally does: 65536 x 512 without
+// groups takes 55 us, 240 with sigmoid logits around -14, 380 around -16 and of equal
+// logits, 440 with a biased softmax equal to 1e-3, 700 with k = 24, 880 with k = 32; 750
+// with 64 groups.
 //
 // Bound by issue: 1003 warp instructions a token of 512 experts with groups, 698
 // without.  65536 x 512, k 10, 4 of 8 groups: 78 us; without groups 55.
@@ -369,7 +378,8 @@ __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k
       a = max2_nan(a, v);
     };
     if constexpr (GROUPED == kEvenGroups) {
-      // straight-line (with the ranks below, 96 -> 90 us at 65536 x 512)
+      // straight-line: 79 us instead of 83 at 65536 x 512 with 8 groups, 53 instead of 57 at
+      // 65536 x 128 with 4
       constexpr int kSteps = NK / 4;
       const float4* part = reinterpret_cast<const float4*>(skey + g * G) + sub;
 #pragma unroll
@@ -416,33 +426,17 @@ __device__ __forceinline__ bool scored_token_fast(const float* row, int E, int k
     // decided by their binary64 scores
     // (maxima on order codes: the integer reduction is one instruction)
     const float big = __uint_as_float(__reduce_max_sync(kFull, __float_as_uint(mag)));
-    uint32_t kept = 0u, best, next;
-    if (GROUPED == kEvenGroups && R.groups <= 8) {
-      // a group's rank: each of its lanes compares it with every unit-th group
-      const uint32_t scode = order_code(score), mine = unit == 32 ? kFull : (1u << unit) - 1u;
-      int rank = 0;
-      for (int j = sub; j < R.groups + sub; j += unit) {
-        const uint32_t other = __shfl_sync(kFull, scode, j << L.shift);
-        const uint32_t above = __ballot_sync(kFull, j < R.groups && other > scode);
-        rank += __popc((above >> (g << L.shift)) & mine);
-      }
-      const bool keep = g < R.groups && rank < R.top_groups;
-      best = __reduce_min_sync(kFull, keep ? scode : 0xffffffffu);
-      next = __reduce_max_sync(kFull, keep || g >= R.groups ? 0u : scode);
-      kept = __reduce_or_sync(kFull, keep ? L.bits : 0u);
-      // (equal scores across the boundary keep more)
-      if (__popc(__ballot_sync(kFull, keep)) != R.top_groups << L.shift) next = best;
-    } else {
-      uint32_t scode = sub == 0 && g < R.groups ? order_code(score) : 0u;
-      best = 0u;
-      for (int r = 0; r < R.top_groups; ++r) {
-        best = __reduce_max_sync(kFull, scode);
-        const int who = __ffs(__ballot_sync(kFull, scode == best)) - 1;
-        kept |= __shfl_sync(kFull, L.bits, who);
-        if (lane == who) scode = 0u;
-      }
-      next = __reduce_max_sync(kFull, scode);
+    // (ranks of the groups, each compared with all others, were no faster for 8 of them, 2 us
+    // slower for 2 and 13 for 32: 65536 x 512)
+    uint32_t kept = 0u, best = 0u;
+    uint32_t scode = sub == 0 && g < R.groups ? order_code(score) : 0u;
+    for (int r = 0; r < R.top_groups; ++r) {
+      best = __reduce_max_sync(kFull, scode);
+      const int who = __ffs(__ballot_sync(kFull, scode == best)) - 1;
+      kept |= __shfl_sync(kFull, L.bits, who);
+      if (lane == who) scode = 0u;
     }
+    const uint32_t next = __reduce_max_sync(kFull, scode);
     if (!(code_float(best) - code_float(next) > 4.0f * bound(big))) {
       const float last = R.group_top == 2 ? b : a;
       const double md = (double)m;

@@ -328,6 +328,11 @@ moe_status_t moe_combine(const moe_shape_t* shape, const void* y, const int32_t*
  *   top_groups 1..groups, with k <= top_groups * (E/groups)
  *   group_top  1 or 2, at most E/groups
  *   scale      finite, > 0
+ * Gates are binary64 quotients rounded once; those of the full softmax
+ * (softmax scores without MOE_F_RENORM) are within 1e-6.
+ * The time depends on the logits: a token whose keys lie closer together than
+ * binary32 tells apart, or with k above about 20 or more than 32 groups, is
+ * decided in binary64, 5 to 15 times slower (csrc/route_scored.cu has which).
  * Buffers as moe_route. */
 #define MOE_SCORE_SOFTMAX 0
 #define MOE_SCORE_SIGMOID 1
@@ -357,7 +362,8 @@ moe_status_t moe_route_scored_backward(const moe_shape_t* shape, const float* lo
  * holds a token of expert e:
  *   z[p,:] = x[p,:] W_e^T + bias_e
  *   y[p,:] = act(z[p,:]) + residual[p,:]
- *   act: none, relu, gelu (by erf), silu, or swiglu: silu(z[:F]) * z[F:]
+ *   act: none, relu, gelu (by erf; far negative values keep their relative
+ *   accuracy), silu, or swiglu: silu(z[:F]) * z[F:]
  * with F = out_features and Wd = F, or 2F with swiglu (rows 0..F-1 of a weight
  * matrix are the gate half, F..2F-1 the up half).
  *   x          bf16 [N,in_features]
